@@ -117,8 +117,11 @@ def sustained(step, stream, seconds: float, device_index: int):
     return {"steps": n, "ms_per_step": a.elapsed_time(b) / n, "clocks": clk.summary()}
 
 
-# device and host sources of the other paths (backward, decode step): edits there leave the forward unchanged
-OTHER_PATH_SOURCES = {"kda_backward.cuh", "kda_backward_api.cuh", "kda_decode.cuh"}
+# device and host sources of the other paths (backward, decode step, softmax attention): edits there leave the
+# forward unchanged
+OTHER_PATH_SOURCES = {"kda_backward.cuh", "kda_backward_api.cuh", "kda_decode.cuh", "kda_lib.cu",
+                      "kda_attn_common.cuh", "kda_attn_api.cuh", "kda_attn_forward.cuh", "kda_attn_backward.cuh",
+                      "kda_attn_decode.cuh", "kda_cache.cuh"}
 
 
 def kernel_source_hash() -> str:

@@ -379,6 +379,35 @@ kda_status_t kda_decode_step(const void *q, int64_t q_row_stride, const void *k,
  */
 kda_status_t kda_l2norm_bf16(const void *x, int64_t rows, int K, void *out, void *stream);
 
+/*
+ * Causal softmax attention over whole prompts, for the full-attention layers
+ * that stand between the gated delta layers.  For a sequence of Lq queries and
+ * Lk keys, query i sees the keys j <= i + Lk - Lq (Lk > Lq: a prefix of keys
+ * comes first; Lk < Lq: the first rows see nothing):
+ *   s_ij = scale q_i . k_j   lse_i = log sum_j exp(s_ij)   o_i = sum_j exp(s_ij - lse_i) v_j
+ * A row that sees no key gets o = 0 and lse = -inf.
+ *   q             bf16, row t (of B * T) at q + t * q_row_stride elements: [H, D]
+ *   k, v          bf16, rows of [HKV, D] (B * Tk of them); query head h reads
+ *                 key/value head h / (H / HKV).  16-byte aligned, strides
+ *                 multiples of 8 elements (a packed QKV row is passed as three
+ *                 pointers with one stride); D = 64 or 128
+ *   cu_seqlens    int32 [num_seqs + 1] device, row offsets of the packed
+ *                 sequences in q, and cu_seqlens_k in k and v (the same
+ *                 pointer where they agree); then B = 1 and num_seqs > 0.  Both
+ *                 null for a plain batch, whose sequences have T and Tk rows.
+ *                 Offsets past the tensors' rows are cut off at them.
+ *   scale         > 0
+ *   o             bf16 [B, T, H, D] out;  lse  fp32 [B, H, T] out.  Rows of no
+ *                 sequence are left as they were, and what they hold (in q, k
+ *                 and v) does not reach a result.
+ * Products are bf16 with fp32 accumulation; the softmax statistics are fp32.
+ * T = 0 is a no-op.  No workspace.  Asynchronous on `stream`.
+ */
+kda_status_t kda_attention_forward(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                   const void *v, int64_t v_row_stride, const int32_t *cu_seqlens,
+                                   const int32_t *cu_seqlens_k, int num_seqs, int B, int T, int Tk, int H, int HKV,
+                                   int D, float scale, void *o, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

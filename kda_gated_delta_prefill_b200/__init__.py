@@ -31,7 +31,7 @@ EXPORTED = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill_forw
             "kda_prefill_backward_workspace_size", "kda_prefill_backward_kernel_launches", "kda_prefill_backward",
             "kda_prefill_state_bf16_workspace_size", "kda_prefill_forward_state_bf16",
             "kda_prefill_forward_save", "kda_prefill_backward_saved", "kda_prefill_forward_varlen",
-            "kda_prefill_varlen_kernel_launches")
+            "kda_prefill_varlen_kernel_launches", "kda_attention_forward")
 
 
 class KdaError(RuntimeError):
@@ -91,6 +91,9 @@ def lib():
         L.kda_prefill_forward_varlen.restype = I
         L.kda_prefill_varlen_kernel_launches.argtypes = [I, I, I, I, I, I, P]
         L.kda_prefill_varlen_kernel_launches.restype = I
+        S, F = ctypes.c_int64, ctypes.c_float
+        L.kda_attention_forward.argtypes = [P, S, P, S, P, S, P, P] + [I] * 7 + [F, P, P, P]
+        L.kda_attention_forward.restype = I
         _lib = L
         return L
 
@@ -448,3 +451,70 @@ def forward_noalloc(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, o=
                B, T, H, HV, K, V, _ptr(o), _ptr(final_state), _stream_ptr(stream, dev))
     _check(rc, "kda_prefill_forward_noalloc")
     return o, final_state
+
+
+def _row_stride(name, t):
+    """Elements between the rows of a [B,T,heads,D] tensor whose rows are compact and evenly spaced."""
+    B, T, heads, D = t.shape
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (heads > 1 and sh != D):
+        raise ValueError(f"{name} must have compact rows")
+    if T > 1:
+        if B > 1 and sb != T * st:
+            raise ValueError(f"{name} must have evenly spaced rows")
+        return st
+    return sb if B > 1 else heads * D
+
+
+def _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, more=()):
+    """Checks of attention over whole prompts; returns (B, T, Tk, H, HKV, D, num_seqs, device, cu_seqlens_k)."""
+    import torch
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B,T,H,D], k and v [B,Tk,HKV,D]")
+    B, T, H, D = q.shape
+    Tk, HKV = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+        raise ValueError("q must be [B,T,H,D], k and v [B,Tk,HKV,D]")
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens
+        if T != Tk and cu_seqlens is not None:
+            raise ValueError("keys of another length than the queries need cu_seqlens_k")
+    elif cu_seqlens is None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    num_seqs = 0
+    if cu_seqlens is not None:
+        num_seqs = cu_seqlens.numel() - 1
+        if num_seqs < 1:
+            raise ValueError("cu_seqlens must hold at least 2 elements")
+    _need_all([("q", q, torch.bfloat16, None, False), ("k", k, torch.bfloat16, None, False),
+               ("v", v, torch.bfloat16, None, False), ("cu_seqlens", cu_seqlens, torch.int32, None, True),
+               ("cu_seqlens_k", cu_seqlens_k, torch.int32, num_seqs + 1, True), *more], q.device)
+    return B, T, Tk, H, HKV, D, num_seqs, q.device, cu_seqlens_k
+
+
+def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, o=None, lse=None, stream=None):
+    """Causal softmax attention over whole prompts (CUDA); returns (o [B,T,H,D] bf16, lse [B,H,T] fp32).
+
+    q: bf16 [B,T,H,D]; k, v: bf16 [B,Tk,HKV,D], H a multiple of HKV, D 64 or 128.  Rows are compact but may be
+    strided (views of a packed QKV tensor).  Query i of a sequence with Lq queries and Lk keys sees the keys
+    j <= i + Lk - Lq; a row that sees none gets o = 0 and lse = -inf.  Packed sequences: B = 1 and cu_seqlens int32
+    [N+1], with cu_seqlens_k where the keys' offsets differ; rows of no sequence are left as they were.
+    scale: D^-0.5 when not given.  lse is the natural logarithm of the row's sum of exponentials.
+    """
+    import torch
+    B, T, Tk, H, HKV, D, num_seqs, dev, cu_k = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
+    if o is None:
+        o = torch.empty(B, T, H, D, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("o", o, torch.bfloat16, B * T * H * D, dev)
+    if lse is None:
+        lse = torch.empty(B, H, T, dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, torch.float32, B * H * T, dev)
+    with _on(dev):
+        rc = lib().kda_attention_forward(_ptr(q), _row_stride("q", q), _ptr(k), _row_stride("k", k), _ptr(v),
+                                         _row_stride("v", v), _ptr(cu_seqlens), _ptr(cu_k), num_seqs, B, T, Tk, H,
+                                         HKV, D, D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse),
+                                         _stream_ptr(stream, dev))
+    _check(rc, "kda_attention_forward")
+    return o, lse

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libkda_prefill.so")
-MAIN_SRC = os.path.join(CSRC, "kda_prefill.cu")
+MAIN_SRC = os.path.join(CSRC, "kda_lib.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,117 @@
+// kda_attn_common.cuh -- what the softmax-attention kernels share: sequence
+// lookup, tensor-core wrappers for bf16 operands, and pair arithmetic.
+#pragma once
+#include "kda_common.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace kda {
+
+// further bits of the device error word
+enum : unsigned { ERR_BLOCK_ID = 16u, ERR_CACHE_FULL = 32u };
+
+constexpr int AT = 128;  // rows of an attention tile, of queries and of keys
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// kind::f16 instruction descriptor: bf16 A and B, fp32 accumulator, either operand MN-major
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? (1u << 15) : 0u) | (b_mn ? (1u << 16) : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] B[smem], called by a whole converged warp (one elected lane issues)
+__device__ __forceinline__ void tc_mma_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+// A [128 rows][D] bf16 tile is D / 64 column halves of [128][64], each 16 KB in the 128-byte-swizzle layout of a
+// TMA load.  K-major (the rows are M or N): 32 bytes further per 16-column step, 16 KB per half.  MN-major (the
+// rows are K): 64-column blocks 16 KB apart, 16-row steps 2 KB apart.
+constexpr int kHalfBytes = AT * 128;
+__device__ __forceinline__ uint64_t tile_desc_k(uint32_t saddr) { return sw128_desc(saddr, 16, 1024); }
+__device__ __forceinline__ uint64_t tile_desc_mn(uint32_t saddr) { return sw128_desc(saddr, kHalfBytes, 1024); }
+__device__ __forceinline__ uint32_t kstep_k(int ks) { return static_cast<uint32_t>((ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2); }
+__device__ __forceinline__ uint32_t kstep_mn(int ks) { return static_cast<uint32_t>(ks * (2048 >> 4)); }
+
+// Rows [first, 128) of a tile become zero (whole warp; the async proxy sees it).  Tail tiles of a sequence hold
+// whatever follows it, and 0 * NaN in a matrix product would carry that into the sequence's results.
+template <int D>
+__device__ __forceinline__ void zero_tail_rows(uint32_t tile, int first, int lane)
+{
+    for (int i = lane; i < (AT - first) * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(
+                             tile + h * kHalfBytes + (first + (i >> 3)) * 128 + (i & 7) * 16),
+                         "r"(0)
+                         : "memory");
+    fence_proxy_async();
+    __syncwarp();
+}
+
+// The sequences of a batch: packed (cu given, clamped to the tensors' rows) or plain.
+struct SeqView {
+    const int32_t *cu_q, *cu_k;  // [N+1], null for a plain batch
+    int N, T, Tk;                // sequences; rows of q and of k (plain: of each sequence)
+};
+struct Seq {
+    int q0, lq, k0, lk;  // first row and length, of queries and of keys
+};
+__device__ __forceinline__ void seq_range(const int32_t *cu, int n, int T, int &first, int &len)
+{
+    const int a = min(max(cu[n], 0), T), b = min(max(cu[n + 1], 0), T);
+    first = a;
+    len = max(b - a, 0);
+}
+__device__ __forceinline__ Seq seq_of(const SeqView &s, int n)
+{
+    Seq r;
+    if (s.cu_q) {
+        seq_range(s.cu_q, n, s.T, r.q0, r.lq);
+        seq_range(s.cu_k, n, s.Tk, r.k0, r.lk);
+    } else {
+        r = Seq{n * s.T, s.T, n * s.Tk, s.Tk};
+    }
+    return r;
+}
+// Blocks of BLK rows are numbered so that no scan of the lengths is needed: sequence n's first block is
+// cu[n] / BLK + n, which leaves room for all of its blocks (and sometimes one that stays empty).
+template <int BLK>
+__host__ __device__ constexpr int block_slots(int N, int T, bool packed)
+{
+    return packed ? T / BLK + N : N * ((T + BLK - 1) / BLK);
+}
+// The sequence and the block in it of slot t; false for an empty slot.  Whole warp; a 32-way search, so two
+// dependent loads find one sequence of a thousand.
+template <int BLK>
+__device__ __forceinline__ bool find_block(const int32_t *cu, int N, int T, int t, int lane, int &n, int &blk)
+{
+    if (!cu) {
+        const int per = (T + BLK - 1) / BLK;
+        n = t / per;
+        blk = t - n * per;
+        return true;
+    }
+    int lo = 0, hi = N;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const bool at = i < hi && min(max(cu[i], 0), T) / BLK + i <= t;
+        const int c = max(__popc(__ballot_sync(0xffffffffu, at)), 1);
+        lo += (c - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    int first, len;
+    seq_range(cu, lo, T, first, len);
+    n = lo;
+    blk = t - (first / BLK + lo);
+    return blk >= 0 && static_cast<int64_t>(blk) * BLK < len;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+}  // namespace kda
