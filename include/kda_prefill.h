@@ -408,6 +408,24 @@ kda_status_t kda_attention_forward(const void *q, int64_t q_row_stride, const vo
                                    const int32_t *cu_seqlens_k, int num_seqs, int B, int T, int Tk, int H, int HKV,
                                    int D, float scale, void *o, float *lse, void *stream);
 
+/*
+ * Gradients of sum(o * dout) for kda_attention_forward on the same inputs,
+ * from the o and lse that it returned (lse itself carries no gradient):
+ *   dq  bf16 [B, T, H, D];  dk, dv  bf16 [B, Tk, HKV, D], summed over the query
+ *       heads that share a key/value head; rows of no sequence stay as they were
+ *   dout  bf16, rows of [H, D] with a row stride, like q
+ *   workspace  16-byte aligned, kda_attention_backward_workspace_size(...)
+ *              bytes (num_seqs 0 for a plain batch); overlaps nothing else
+ * Every sum has one owner and a fixed order: the same bits on every run.
+ */
+size_t kda_attention_backward_workspace_size(int B, int T, int H, int num_seqs);
+kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                    const void *v, int64_t v_row_stride, const void *o, const float *lse,
+                                    const void *dout, int64_t dout_row_stride, const int32_t *cu_seqlens,
+                                    const int32_t *cu_seqlens_k, int num_seqs, int B, int T, int Tk, int H, int HKV,
+                                    int D, float scale, void *dq, void *dk, void *dv, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

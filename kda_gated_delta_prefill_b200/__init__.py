@@ -31,7 +31,8 @@ EXPORTED = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill_forw
             "kda_prefill_backward_workspace_size", "kda_prefill_backward_kernel_launches", "kda_prefill_backward",
             "kda_prefill_state_bf16_workspace_size", "kda_prefill_forward_state_bf16",
             "kda_prefill_forward_save", "kda_prefill_backward_saved", "kda_prefill_forward_varlen",
-            "kda_prefill_varlen_kernel_launches", "kda_attention_forward")
+            "kda_prefill_varlen_kernel_launches", "kda_attention_forward",
+            "kda_attention_backward_workspace_size", "kda_attention_backward")
 
 
 class KdaError(RuntimeError):
@@ -94,6 +95,10 @@ def lib():
         S, F = ctypes.c_int64, ctypes.c_float
         L.kda_attention_forward.argtypes = [P, S, P, S, P, S, P, P] + [I] * 7 + [F, P, P, P]
         L.kda_attention_forward.restype = I
+        L.kda_attention_backward_workspace_size.argtypes = [I] * 4
+        L.kda_attention_backward_workspace_size.restype = Z
+        L.kda_attention_backward.argtypes = [P, S, P, S, P, S, P, P, P, S, P, P] + [I] * 7 + [F, P, P, P, P, Z, P]
+        L.kda_attention_backward.restype = I
         _lib = L
         return L
 
@@ -518,3 +523,35 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
                                          _stream_ptr(stream, dev))
     _check(rc, "kda_attention_forward")
     return o, lse
+
+
+def attention_backward_workspace_size(B, T, H, num_seqs=0) -> int:
+    return int(lib().kda_attention_backward_workspace_size(B, T, H, num_seqs))
+
+
+def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, workspace=None,
+                       stream=None):
+    """Gradients of sum(o * dout) for ``attention_forward`` on the same inputs, from the o and lse it returned (CUDA).
+
+    Returns (dq [B,T,H,D], dk, dv [B,Tk,HKV,D]) in bf16; dk and dv are summed over the query heads that share a
+    key/value head.  dout's rows may be strided like q's.  Rows of no sequence are not written.
+    """
+    import torch
+    B, T, Tk, H, HKV, D, num_seqs, dev, cu_k = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
+    if dout.dim() != 4 or dout.shape != q.shape:
+        raise ValueError("dout must be [B,T,H,D]")
+    _need_all([("o", o, torch.bfloat16, B * T * H * D, True), ("lse", lse, torch.float32, B * H * T, True),
+               ("dout", dout, torch.bfloat16, None, False), ("workspace", workspace, torch.uint8, None, True)], dev)
+    dq = torch.empty(B, T, H, D, dtype=torch.bfloat16, device=dev)
+    dk = torch.empty(B, Tk, HKV, D, dtype=torch.bfloat16, device=dev)
+    dv = torch.empty(B, Tk, HKV, D, dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        workspace = torch.empty(attention_backward_workspace_size(B, T, H, num_seqs), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        rc = lib().kda_attention_backward(_ptr(q), _row_stride("q", q), _ptr(k), _row_stride("k", k), _ptr(v),
+                                          _row_stride("v", v), _ptr(o), _ptr(lse), _ptr(dout),
+                                          _row_stride("dout", dout), _ptr(cu_seqlens), _ptr(cu_k), num_seqs, B, T, Tk,
+                                          H, HKV, D, D ** -0.5 if scale is None else scale, _ptr(dq), _ptr(dk),
+                                          _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, dev))
+    _check(rc, "kda_attention_backward")
+    return dq, dk, dv

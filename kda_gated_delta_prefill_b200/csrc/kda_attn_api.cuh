@@ -1,6 +1,7 @@
 // kda_attn_api.cuh -- C ABI of the softmax-attention operators (declared in
 // include/kda_prefill.h): host-side argument checks, tensor maps, launches.
 #pragma once
+#include "kda_attn_backward.cuh"
 #include "kda_attn_forward.cuh"
 
 namespace {
@@ -89,7 +90,8 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
     if (st != KDA_OK) return st;
     if (d.rows == 0) return KDA_OK;
     const int64_t wq = static_cast<int64_t>(H) * D, wk = static_cast<int64_t>(HKV) * D;
-    if ((st = check_rows(q, d.rows, q_row_stride, wq)) != KDA_OK || (st = check_rows(k, d.krows, k_row_stride, wk)) != KDA_OK ||
+    if ((st = check_rows(q, d.rows, q_row_stride, wq)) != KDA_OK ||
+        (st = check_rows(k, d.krows, k_row_stride, wk)) != KDA_OK ||
         (st = check_rows(v, d.krows, v_row_stride, wk)) != KDA_OK)
         return st;
     if (!o || !lse) return KDA_ERR_INVALID_ARG;
@@ -129,4 +131,86 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
     };
     return D == 128 ? launch(kda_attn_fwd_kernel<128>, AttnFwdSmem<128>::TOTAL)
                     : launch(kda_attn_fwd_kernel<64>, AttnFwdSmem<64>::TOTAL);
+}
+
+extern "C" size_t kda_attention_backward_workspace_size(int B, int T, int H, int num_seqs)
+{
+    if (B <= 0 || T < 0 || H <= 0 || num_seqs < 0 || (num_seqs > 0 && B != 1)) return 0;
+    const int64_t slots = num_seqs > 0 ? static_cast<int64_t>(T) / kda::AT + num_seqs
+                                       : static_cast<int64_t>(B) * ((static_cast<int64_t>(T) + kda::AT - 1) / kda::AT);
+    return static_cast<size_t>(slots) * H * 2 * kda::AT * sizeof(float);
+}
+
+extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                                               const void *v, int64_t v_row_stride, const void *o, const float *lse,
+                                               const void *dout, int64_t dout_row_stride, const int32_t *cu_seqlens,
+                                               const int32_t *cu_seqlens_k, int num_seqs, int B, int T, int Tk, int H,
+                                               int HKV, int D, float scale, void *dq, void *dk, void *dv,
+                                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    AttnDims d;
+    kda_status_t st = attn_dims(B, T, Tk, H, HKV, D, scale, cu_seqlens, cu_seqlens_k, num_seqs, d);
+    if (st != KDA_OK) return st;
+    const int64_t wq = static_cast<int64_t>(H) * D, wk = static_cast<int64_t>(HKV) * D;
+    if ((st = check_rows(q, d.rows, q_row_stride, wq)) != KDA_OK ||
+        (st = check_rows(k, d.krows, k_row_stride, wk)) != KDA_OK ||
+        (st = check_rows(v, d.krows, v_row_stride, wk)) != KDA_OK || (st = check_rows(o, d.rows, wq, wq)) != KDA_OK ||
+        (st = check_rows(dout, d.rows, dout_row_stride, wq)) != KDA_OK)
+        return st;
+    if ((d.rows && (!lse || !dq || !workspace)) || (d.krows && (!dk || !dv))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(lse, 4) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(workspace, 16))
+        return KDA_ERR_MISALIGNED;
+    const size_t need = kda_attention_backward_workspace_size(B, T, H, num_seqs);
+    if (d.rows && workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    const size_t ncu = static_cast<size_t>(d.N + 1) * 4, nq = span(d.rows, wq, wq, 2), nk = span(d.krows, wk, wk, 2);
+    const Range out[] = {{dq, nq}, {dk, nk}, {dv, nk}, {workspace, need}};
+    const Range in[] = {{q, span(d.rows, q_row_stride, wq, 2)}, {k, span(d.krows, k_row_stride, wk, 2)},
+                        {v, span(d.krows, v_row_stride, wk, 2)}, {o, nq},
+                        {lse, static_cast<size_t>(d.rows) * H * 4}, {dout, span(d.rows, dout_row_stride, wq, 2)},
+                        {cu_seqlens, ncu}, {cu_seqlens_k, ncu}};
+    if (outputs_overlap(out, in)) return KDA_ERR_INVALID_ARG;
+    if (d.rows == 0 && d.krows == 0) return KDA_OK;
+
+    DeviceInfo info;
+    if (device_info(info) != cudaSuccess) return KDA_ERR_CUDA;
+    using namespace kda;
+    AttnBwdParams p{};
+    p.seq = SeqView{cu_seqlens, cu_seqlens_k, d.N, T, Tk};
+    p.H = H;
+    p.HKV = HKV;
+    p.qslots = block_slots<AT>(d.N, T, d.packed);
+    p.kslots = block_slots<AT>(d.N, Tk, d.packed);
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.o = static_cast<const __nv_bfloat16 *>(o);
+    p.dout = static_cast<const __nv_bfloat16 *>(dout);
+    p.do_stride = dout_row_stride;
+    p.lse = lse;
+    p.stats = static_cast<float *>(workspace);
+    p.dq = static_cast<__nv_bfloat16 *>(dq);
+    p.dk = static_cast<__nv_bfloat16 *>(dk);
+    p.dv = static_cast<__nv_bfloat16 *>(dv);
+    p.err = info.err;
+    CUtensorMap mq, mk, mv, mdo;
+    if (d.rows && (!attn_map(&mq, q, H, d.rows, q_row_stride, D) || !attn_map(&mdo, dout, H, d.rows, dout_row_stride, D)))
+        return KDA_ERR_CUDA;
+    if (d.krows && (!attn_map(&mk, k, HKV, d.krows, k_row_stride, D) || !attn_map(&mv, v, HKV, d.krows, v_row_stride, D)))
+        return KDA_ERR_CUDA;
+    // a side without rows: the kernels write zeros to the other side's gradients and load nothing
+    if (!d.rows) mq = mdo = mk;
+    if (!d.krows) mk = mv = mq;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto run = [&](auto stats, auto dkv, int dkv_smem, auto dqk, int dq_smem) {
+        if (cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem) != cudaSuccess ||
+            cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        if (d.rows) stats<<<p.qslots * H, kAttnStatThreads, 0, s>>>(p);
+        if (d.krows) dkv<<<p.kslots * HKV, kAttnBwdThreads, dkv_smem, s>>>(p, mq, mk, mv, mdo);
+        if (d.rows) dqk<<<p.qslots * H, kAttnBwdThreads, dq_smem, s>>>(p, mq, mk, mv, mdo);
+        return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    };
+    return D == 128 ? run(kda_attn_stats_kernel<128>, kda_attn_dkv_kernel<128>, AttnDkvSmem<128>::TOTAL,
+                          kda_attn_dq_kernel<128>, AttnDqSmem<128>::TOTAL)
+                    : run(kda_attn_stats_kernel<64>, kda_attn_dkv_kernel<64>, AttnDkvSmem<64>::TOTAL,
+                          kda_attn_dq_kernel<64>, AttnDqSmem<64>::TOTAL);
 }

@@ -1,0 +1,546 @@
+// kda_attn_backward.cuh -- gradients of causal softmax attention, on the
+// 5th-generation tensor cores.
+//
+// With P_ij = exp(s_ij - lse_i) and delta_i = o_i . do_i (= sum_j P_ij dP_ij):
+//   dV_j = sum_i P_ij do_i          dP_ij = do_i . v_j          dS_ij = P_ij (dP_ij - delta_i)
+//   dQ_i = scale sum_j dS_ij k_j    dK_j = scale sum_i dS_ij q_i
+// dK and dV of a shared key/value head are sums over its query heads.
+//
+// Three launches: the statistics (delta, and lse in units of log 2, in tiles of 128 rows), dK/dV, and dQ.  dK/dV walks
+// the queries for a tile of keys and dQ the keys for a tile of queries, so every sum has one owner and a fixed
+// order: no atomics, the same bits every time.  The price is that S and dP are formed twice (7 matrix products
+// instead of 5).
+//
+// dK/dV works on the transposes: a thread owns a key row of S^T = K Q^T and dP^T = V dO^T, so P^T and dS^T go back to
+// TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
+// TMEM (D = 128): S^T/P^T, dP^T/dS^T, dV, dK with 128 columns each.  The order of the MMAs,
+//   dV(i), S^T(i+1), dK(i), dP^T(i+1), dV(i+1), ...
+// leaves two products' time for each of P (between S^T and dV) and dS (between dP^T and dK).
+#pragma once
+#include "kda_attn_common.cuh"
+
+namespace kda {
+
+struct AttnBwdParams {
+    SeqView seq;
+    int H, HKV, qslots, kslots;  // slots of 128 rows of q and of k
+    float scale, scale_log2;
+    const __nv_bfloat16 *o, *dout;
+    int64_t do_stride;
+    const float *lse;
+    float *stats;  // [H][qslots][2][128]: lse * log2(e) (+inf: no probability), delta
+    __nv_bfloat16 *dq, *dk, *dv;
+    unsigned *err;
+};
+
+// ---------------------------------------------------------------------------------------------------- statistics
+// A warp per row: bound by reading o and dout once.
+constexpr int kAttnStatThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kAttnStatThreads) kda_attn_stats_kernel(const AttnBwdParams p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
+    int n, blk;
+    if (!find_block<AT>(p.seq.cu_q, p.seq.N, p.seq.T, slot, lane, n, blk)) return;
+    const Seq sq = seq_of(p.seq, n);
+    float *out = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
+    constexpr int R = AT / (kAttnStatThreads / 32);
+    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp at a time
+    for (int i = 0; i < R; i += RPW) {
+        const int r = warp * R + i + lane / LPR, row = blk * AT + r;
+        float s = 0.f;
+        if (row < sq.lq) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p.o + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D +
+                                                             8 * (lane % LPR));
+            const uint4 b = *reinterpret_cast<const uint4 *>(p.dout + (static_cast<int64_t>(sq.q0) + row) * p.do_stride +
+                                                             h * D + 8 * (lane % LPR));
+            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += bf16lo(x[e]) * bf16lo(y[e]) + bf16hi(x[e]) * bf16hi(y[e]);
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane % LPR == 0) {
+            float l2 = INFINITY;
+            if (row < sq.lq) {
+                const int64_t at = p.seq.cu_q ? static_cast<int64_t>(h) * p.seq.T + sq.q0 + row
+                                              : (static_cast<int64_t>(n) * p.H + h) * p.seq.T + row;
+                l2 = p.lse[at] == -INFINITY ? INFINITY : p.lse[at] * kLog2e;
+            }
+            out[r] = l2;
+            out[AT + r] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------- dK and dV
+template <int D>
+struct AttnDkvSmem {
+    static constexpr int TILE = AT * D * 2;
+    static constexpr int NST = D == 128 ? 2 : 4;
+    static constexpr int Q = 2 * TILE;              // K, V, then the rings of Q, dO and statistics
+    static constexpr int DO = Q + NST * TILE;
+    static constexpr int STAT = DO + NST * TILE;
+    static constexpr int BAR = STAT + NST * 1024;   // qfull qempty dofull doempty [NST], kfull vfull sfull pready dpfull dsready done
+    static constexpr int TMEM_SLOT = BAR + (4 * NST + 7) * 8;
+    static constexpr int ABORT = TMEM_SLOT + 4;
+    static constexpr int TOTAL = ABORT + 4;
+};
+// 8 warps of arithmetic, one of MMAs, one of loads, two idle: three warpgroups for the register split
+// (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int kAttnBwdThreads = 384;
+
+template <int D>
+__global__ void __launch_bounds__(kAttnBwdThreads, 1)
+    kda_attn_dkv_kernel(const AttnBwdParams p, const __grid_constant__ CUtensorMap mq,
+                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                        const __grid_constant__ CUtensorMap mdo)
+{
+    using S = AttnDkvSmem<D>;
+    constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
+    constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = blockIdx.x % p.HKV, slot = blockIdx.x / p.HKV, G = p.H / p.HKV;
+    int n, blk;
+    if (!find_block<AT>(p.seq.cu_k, p.seq.N, p.seq.Tk, slot, lane, n, blk)) return;
+    const Seq sq = seq_of(p.seq, n);
+    const int diff = sq.lk - sq.lq, j0 = blk * AT;
+    // query tiles that see a key of this tile: first .. nq - 1 of every head of the group
+    const int nq = (sq.lq + AT - 1) / AT, first = j0 > diff ? (j0 - diff) / AT : 0;
+    const int cnt = max(nq - first, 0), total = cnt * G;
+    const int qslot0 = p.seq.cu_q ? sq.q0 / AT + n : n * nq;  // the sequence's first slot of statistics
+
+    const uint32_t qfull = sb + S::BAR, qempty = qfull + 8 * NST, dofull = qempty + 8 * NST, doempty = dofull + 8 * NST,
+                   kfull = doempty + 8 * NST, vfull = kfull + 8, sfull = kfull + 16, pready = kfull + 24,
+                   dpfull = kfull + 32, dsready = kfull + 40, done = kfull + 48;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
+    if (tid == 0) {
+        for (int s = 0; s < 4 * NST; ++s) mbar_init(qfull + 8 * s, 1);
+        for (uint32_t b : {kfull, vfull, sfull, dpfull, done}) mbar_init(b, 1);
+        mbar_init(pready, 8);
+        mbar_init(dsready, 8);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + S::TMEM_SLOT);
+    auto fail = [&](unsigned code) {
+        atomicOr(p.err, code);
+        *abort_flag = 1;
+    };
+
+    if (warp < 8) {
+        // ---------------- P^T and dS^T: key row, half of the query columns ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
+        const uint32_t ts = tmem + lb + TM_S + 64 * half, td = tmem + lb + TM_DP + 64 * half;
+        const int key = j0 + 32 * quarter + lane;
+        const float c = p.scale_log2;
+        bool ok = true;
+        for (int it = 0; it < total; ++it) {
+            const int i = first + it % cnt, st = it % NST;
+            ok = mbar_wait_spin(qfull + 8 * st, (it / NST) & 1) && mbar_wait_spin(sfull, it & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t r[2][32];
+            tc_ld32(ts, r[0]);
+            tc_ld32(ts + 32, r[1]);
+            const float4 *l2 = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 16 * half;
+            const float4 *dl = l2 + 32;
+            tc_wait_ld();
+            // queries q >= key - diff see the key
+            const int from = key - diff - i * AT - 64 * half;
+            const bool cut = __any_sync(0xffffffffu, from > 0);
+            float2 pr[32];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float4 l = l2[e];
+                uint32_t *x = &r[e >> 3][4 * (e & 7)];
+                float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c, c),
+                                make_float2(-l.x, -l.y));
+                float2 b = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c, c),
+                                make_float2(-l.z, -l.w));
+                a = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
+                b = make_float2(ex2_ftz(b.x), ex2_ftz(b.y));
+                if (cut) {
+                    if (4 * e < from) a.x = 0.f;
+                    if (4 * e + 1 < from) a.y = 0.f;
+                    if (4 * e + 2 < from) b.x = 0.f;
+                    if (4 * e + 3 < from) b.y = 0.f;
+                }
+                pr[2 * e] = a;
+                pr[2 * e + 1] = b;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(pr[16 * k + e].x, pr[16 * k + e].y);
+                tc_st16(ts + 16 * k, w);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pready);
+
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(dpfull, it & 1));
+            if (!ok) break;
+            tc_fence_after();
+            tc_ld32(td, r[0]);
+            tc_ld32(td + 32, r[1]);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 d4 = dl[8 * k + e];
+                    const uint32_t *x = &r[k][4 * e];
+                    const float2 a = mul2(pr[16 * k + 2 * e],
+                                          add2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                               make_float2(-d4.x, -d4.y)));
+                    const float2 b = mul2(pr[16 * k + 2 * e + 1],
+                                          add2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                               make_float2(-d4.z, -d4.w)));
+                    w[2 * e] = pack_bf16(a.x, a.y);
+                    w[2 * e + 1] = pack_bf16(b.x, b.y);
+                }
+                tc_st16(td + 16 * k, w);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dsready);
+        }
+        if (ok && total > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(done, 0));
+        if (!ok) {
+            if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
+        } else {
+            // warps 0-3 store dV, 4-7 dK, through the K and V tiles (no MMA reads them any more)
+            tc_fence_after();
+            const int row = j0 + 32 * quarter;
+            const int64_t at = ((static_cast<int64_t>(sq.k0) + row) * p.HKV + hk) * D;
+            store_rows<D>(tmem + lb + (half ? TM_DK : TM_DV), total > 0, half ? p.scale : 1.f,
+                          sb + half * TILE + quarter * (32 * D * 2), lane, sq.lk - row, (half ? p.dk : p.dv) + at,
+                          static_cast<int64_t>(p.HKV) * D);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (warp == 9 && lane == 0 && total > 0) {
+            // ---------------- loads ----------------
+            int nqi = 0, ndo = 0;  // tiles of Q and of dO requested
+            bool ok = true;
+            auto tile = [&](const CUtensorMap *m, uint32_t dst, int head, int row, uint32_t bar) {
+                for (int c = 0; c < HALVES; ++c) tma_load_3d(dst + c * kHalfBytes, m, 64 * c, head, row, bar);
+            };
+            mbar_expect_tx(kfull, TILE);
+            tile(&mk, sb, hk, sq.k0 + j0, kfull);
+            for (int it = 0; it < total && ok && !*abort_flag; ++it) {
+                const int hq = hk * G + it / cnt, i = first + it % cnt, st = it % NST;
+                const uint32_t par = ((it / NST) - 1) & 1;
+                if (it >= NST && !mbar_wait(qempty + 8 * st, par)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(qfull + 8 * st, TILE + 1024);
+                tile(&mq, sb + S::Q + st * TILE, hq, sq.q0 + i * AT, qfull + 8 * st);
+                bulk_load(sb + S::STAT + st * 1024,
+                          p.stats + (static_cast<int64_t>(hq) * p.qslots + qslot0 + i) * (2 * AT), 1024, qfull + 8 * st);
+                ++nqi;
+                if (it == 0) {
+                    mbar_expect_tx(vfull, TILE);
+                    tile(&mv, sb + TILE, hk, sq.k0 + j0, vfull);
+                }
+                if (it >= NST && !mbar_wait(doempty + 8 * st, par)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(dofull + 8 * st, TILE);
+                tile(&mdo, sb + S::DO + st * TILE, hq, sq.q0 + i * AT, dofull + 8 * st);
+                ++ndo;
+            }
+            if (!ok) fail(ERR_PIPE_EMPTY_WAIT);
+            if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
+                mbar_wait(kfull, 0);
+                if (nqi) mbar_wait(vfull, 0);
+                for (int i = max(0, nqi - NST); i < nqi; ++i) mbar_wait(qfull + 8 * (i % NST), (i / NST) & 1);
+                for (int i = max(0, ndo - NST); i < ndo; ++i) mbar_wait(dofull + 8 * (i % NST), (i / NST) & 1);
+            }
+        } else if (warp == 8 && total > 0) {
+            // ---------------- MMAs ----------------
+            const uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
+            const uint64_t kd = tile_desc_k(sb), vd = tile_desc_k(sb + TILE);
+            const uint64_t qk = tile_desc_k(sb + S::Q), dok = tile_desc_k(sb + S::DO);
+            const uint64_t qm = tile_desc_mn(sb + S::Q), dom = tile_desc_mn(sb + S::DO);
+            const int tail = sq.lq - (nq - 1) * AT;  // rows of the last query tile
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
+                tc_fence_after();
+                return ok;
+            };
+            auto score = [&](int it) {  // S^T = K Q^T
+                const int st = it % NST;
+                if (!wait(qfull + 8 * st, (it / NST) & 1)) return;
+                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + S::Q + st * TILE, tail, lane);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_ss_warp(tmem + TM_S, kd + kstep_k(ks), qk + st * (TILE >> 4) + kstep_k(ks), id_s, ks > 0);
+                tc_commit_warp(sfull);
+            };
+            auto dprob = [&](int it) {  // dP^T = V dO^T
+                const int st = it % NST;
+                if (!wait(dofull + 8 * st, (it / NST) & 1)) return;
+                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + S::DO + st * TILE, tail, lane);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_ss_warp(tmem + TM_DP, vd + kstep_k(ks), dok + st * (TILE >> 4) + kstep_k(ks), id_s, ks > 0);
+                tc_commit_warp(dpfull);
+            };
+            // D += A B with A's halves of 64 columns (32 words) at a and a + 64
+            auto accumulate = [&](uint32_t d, uint32_t a, uint64_t b, bool more) {
+#pragma unroll
+                for (int ks = 0; ks < AT / 16; ++ks)
+                    tc_mma_ts_warp(d, a + (ks >> 2) * 64 + (ks & 3) * 8, b + kstep_mn(ks), id_d, more || ks > 0);
+            };
+            if (wait(kfull, 0)) score(0);
+            if (wait(vfull, 0)) dprob(0);
+            for (int it = 0; it < total && ok && !__any_sync(0xffffffffu, *abort_flag); ++it) {
+                const int st = it % NST;
+                if (!wait(pready, it & 1)) break;
+                accumulate(tmem + TM_DV, tmem + TM_S, dom + st * (TILE >> 4), it > 0);
+                tc_commit_warp(doempty + 8 * st);
+                if (it + 1 < total) score(it + 1);
+                if (!wait(dsready, it & 1)) break;
+                accumulate(tmem + TM_DK, tmem + TM_DP, qm + st * (TILE >> 4), it > 0);
+                tc_commit_warp(qempty + 8 * st);
+                if (it + 1 < total) dprob(it + 1);
+            }
+            tc_commit_warp(done);
+            if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tc_dealloc(tmem, TM_COLS);
+}
+
+// ---------------------------------------------------------------------------------------------------- dQ
+// One CTA per tile of 128 queries of a head; a thread owns a query row of S and dP.  TMEM: S in two buffers (dS in
+// bf16 over the one it came from), dP, dQ.  S of the next key tile is formed while this one's exponentials run, and
+// dP of the next while P of the next is formed.
+template <int D>
+struct AttnDqSmem {
+    static constexpr int TILE = AT * D * 2;
+    static constexpr int NST = D == 128 ? 5 : 8;
+    static constexpr int RING = 2 * TILE;           // Q, dO, then K_0, V_0, K_1, V_1, ...
+    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready done
+    static constexpr int TMEM_SLOT = BAR + (2 * NST + 7) * 8;
+    static constexpr int ABORT = TMEM_SLOT + 4;
+    static constexpr int TOTAL = ABORT + 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAttnBwdThreads, 1)
+    kda_attn_dq_kernel(const AttnBwdParams p, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mdo)
+{
+    using S = AttnDqSmem<D>;
+    constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
+    constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % p.H, slot = p.qslots - 1 - blockIdx.x / p.H;
+    int n, blk;
+    if (!find_block<AT>(p.seq.cu_q, p.seq.N, p.seq.T, slot, lane, n, blk)) return;
+    const Seq sq = seq_of(p.seq, n);
+    const int diff = sq.lk - sq.lq, r0 = blk * AT;
+    const int seen_tile = min(r0 + AT, sq.lq) + diff;  // keys that the tile's last row sees
+    const int nt = seen_tile <= 0 ? 0 : (seen_tile + AT - 1) / AT;
+
+    const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull = empty0 + 8 * NST, dofull = qfull + 8,
+                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready = qfull + 40, done = qfull + 48;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
+    if (tid == 0) {
+        for (int s = 0; s < 2 * NST; ++s) mbar_init(full0 + 8 * s, 1);
+        for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull, done}) mbar_init(b, 1);
+        mbar_init(dsready, 8);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + S::TMEM_SLOT);
+    auto fail = [&](unsigned code) {
+        atomicOr(p.err, code);
+        *abort_flag = 1;
+    };
+
+    if (warp < 8) {
+        // ---------------- P and dS: query row, half of the key columns ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        const int half = warp >> 2, quarter = warp & 3;
+        const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
+        const uint32_t td = tmem + lb + TM_DP + 64 * half;
+        const int r = 32 * quarter + lane;
+        const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
+        const float l2 = stat[r], delta = stat[AT + r];
+        const int seen = r0 + r + 1 + diff - 64 * half;  // keys of this half that the row sees (rows past the end: p = 0)
+        const float c = p.scale_log2;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            const uint32_t ts = tmem + lb + TM_S + 128 * (j & 1) + 64 * half;
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(sfull0 + 8 * (j & 1), (j >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[2][32];
+            tc_ld32(ts, x[0]);
+            tc_ld32(ts + 32, x[1]);
+            tc_wait_ld();
+            const int keys = seen - j * AT;
+            const bool cut = __any_sync(0xffffffffu, keys < 64);
+            float2 pr[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const uint32_t *y = &x[e >> 4][2 * (e & 15)];
+                float2 a = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), make_float2(c, c),
+                                make_float2(-l2, -l2));
+                a = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
+                if (cut) {
+                    if (2 * e >= keys) a.x = 0.f;
+                    if (2 * e + 1 >= keys) a.y = 0.f;
+                }
+                pr[e] = a;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(dpfull, j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            tc_ld32(td, x[0]);
+            tc_ld32(td + 32, x[1]);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 a = mul2(pr[16 * k + e], add2(make_float2(__uint_as_float(x[k][2 * e]),
+                                                                           __uint_as_float(x[k][2 * e + 1])),
+                                                               make_float2(-delta, -delta)));
+                    w[e] = pack_bf16(a.x, a.y);
+                }
+                tc_st16(ts + 16 * k, w);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dsready);
+        }
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(done, 0));
+        if (!ok) {
+            if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
+        } else if (half == 0) {
+            // through the Q tile (no MMA reads it any more)
+            tc_fence_after();
+            const int row = r0 + 32 * quarter;
+            store_rows<D>(tmem + lb + TM_DQ, nt > 0, p.scale, sb + quarter * (32 * D * 2), lane, sq.lq - row,
+                          p.dq + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D, static_cast<int64_t>(p.H) * D);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (warp == 9 && lane == 0 && nt > 0) {
+            // ---------------- loads ----------------
+            const int hk = h / (p.H / p.HKV);
+            bool ok = true;
+            auto tile = [&](const CUtensorMap *m, uint32_t dst, int head, int row, uint32_t bar) {
+                mbar_expect_tx(bar, TILE);
+                for (int c = 0; c < HALVES; ++c) tma_load_3d(dst + c * kHalfBytes, m, 64 * c, head, row, bar);
+            };
+            tile(&mq, sb, h, sq.q0 + r0, qfull);
+            int issued = 0;
+            for (; issued < 2 * nt && !*abort_flag; ++issued) {
+                const int s = issued % NST;
+                if (issued >= NST && !mbar_wait(empty0 + 8 * s, ((issued / NST) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tile(issued & 1 ? &mv : &mk, sb + S::RING + s * TILE, hk, sq.k0 + (issued >> 1) * AT, full0 + 8 * s);
+                if (issued == 0) tile(&mdo, sb + TILE, h, sq.q0 + r0, dofull);
+            }
+            if (!ok) fail(ERR_PIPE_EMPTY_WAIT);
+            if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
+                mbar_wait(qfull, 0);
+                if (issued) mbar_wait(dofull, 0);
+                for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
+            }
+        } else if (warp == 8 && nt > 0) {
+            // ---------------- MMAs ----------------
+            const uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
+            const uint64_t qd = tile_desc_k(sb), dod = tile_desc_k(sb + TILE);
+            const uint64_t rk = tile_desc_k(sb + S::RING), rm = tile_desc_mn(sb + S::RING);
+            const int tail = sq.lk - (nt - 1) * AT;  // rows of the last key tile, if fewer than 128
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
+                tc_fence_after();
+                return ok;
+            };
+            // the tile at a ring position, with what follows the sequence taken out
+            auto arrived = [&](int pos) {
+                if (!wait(full0 + 8 * (pos % NST), (pos / NST) & 1)) return false;
+                if (tail < AT && (pos >> 1) == nt - 1) zero_tail_rows<D>(sb + S::RING + (pos % NST) * TILE, tail, lane);
+                return true;
+            };
+            auto product = [&](uint32_t d, uint64_t a, int pos) {
+                const uint64_t b = rk + (pos % NST) * (TILE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_ss_warp(d, a + kstep_k(ks), b + kstep_k(ks), id_s, ks > 0);
+            };
+            auto score = [&](int j) {  // S = Q K^T
+                if (!arrived(2 * j)) return;
+                product(tmem + TM_S + 128 * (j & 1), qd, 2 * j);
+                tc_commit_warp(sfull0 + 8 * (j & 1));
+            };
+            auto dprob = [&](int j) {  // dP = dO V^T
+                if (!arrived(2 * j + 1)) return;
+                product(tmem + TM_DP, dod, 2 * j + 1);
+                tc_commit_warp(dpfull);
+                tc_commit_warp(empty0 + 8 * ((2 * j + 1) % NST));
+            };
+            if (wait(qfull, 0)) score(0);
+            if (wait(dofull, 0)) dprob(0);
+            if (ok && nt > 1) score(1);
+            for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+                if (!wait(dsready, j & 1)) break;
+                const uint64_t b = rm + ((2 * j) % NST) * (TILE >> 4);
+                const uint32_t a = tmem + TM_S + 128 * (j & 1);
+                if (j + 1 < nt) dprob(j + 1);
+#pragma unroll
+                for (int ks = 0; ks < AT / 16; ++ks)
+                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 2) * 64 + (ks & 3) * 8, b + kstep_mn(ks), id_d,
+                                   j > 0 || ks > 0);
+                tc_commit_warp(empty0 + 8 * ((2 * j) % NST));
+                if (ok && j + 2 < nt) score(j + 2);
+            }
+            tc_commit_warp(done);
+            if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tc_dealloc(tmem, TM_COLS);
+}
+
+}  // namespace kda

@@ -35,7 +35,10 @@ __device__ __forceinline__ void tc_mma_ss_warp(uint32_t d_tmem, uint64_t a_desc,
 constexpr int kHalfBytes = AT * 128;
 __device__ __forceinline__ uint64_t tile_desc_k(uint32_t saddr) { return sw128_desc(saddr, 16, 1024); }
 __device__ __forceinline__ uint64_t tile_desc_mn(uint32_t saddr) { return sw128_desc(saddr, kHalfBytes, 1024); }
-__device__ __forceinline__ uint32_t kstep_k(int ks) { return static_cast<uint32_t>((ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2); }
+__device__ __forceinline__ uint32_t kstep_k(int ks)
+{
+    return static_cast<uint32_t>((ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2);
+}
 __device__ __forceinline__ uint32_t kstep_mn(int ks) { return static_cast<uint32_t>(ks * (2048 >> 4)); }
 
 // Rows [first, 128) of a tile become zero (whole warp; the async proxy sees it).  Tail tiles of a sequence hold
@@ -110,6 +113,50 @@ __device__ __forceinline__ bool find_block(const int32_t *cu, int N, int T, int 
     n = lo;
     blk = t - (first / BLK + lo);
     return blk >= 0 && static_cast<int64_t>(blk) * BLK < len;
+}
+
+// The warp's 32 rows of a [128 rows][D] fp32 accumulator (TMEM, row = lane), times mul, rounded to bf16 and stored
+// to dst + row * stride for the first `rows` of them, through 32 * D * 2 bytes of shared memory so that the global
+// accesses are whole rows.  Without `any` the rows are zeros and TMEM is not read; a row whose mul is 0 is zeros.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, uint32_t stage, int lane, int rows,
+                                           __nv_bfloat16 *dst, int64_t stride)
+{
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        uint32_t v[32];
+        if (any) {
+            tc_ld32(taddr + 32 * i, v);
+            tc_wait_ld();
+        }
+        const bool zero = !any || mul == 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                u[k] = zero ? 0u
+                            : pack_bf16(__uint_as_float(v[8 * e + 2 * k]) * mul,
+                                        __uint_as_float(v[8 * e + 2 * k + 1]) * mul);
+            const int ch = 4 * i + e;  // 16-byte piece of the row, swizzled by the row
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(stage + lane * (D * 2) +
+                                                                           ((ch ^ (lane & 7)) << 4)),
+                         "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                         : "memory");
+        }
+    }
+    __syncwarp();
+    constexpr int PER = D * 2 / 16, ROWS = 32 / PER;  // pieces of a row, rows of one warp access
+#pragma unroll
+    for (int i = 0; i < 32 / ROWS; ++i) {
+        const int rr = i * ROWS + lane / PER, ch = lane % PER;
+        if (rr >= rows) continue;
+        uint4 u;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(stage + rr * (D * 2) + ((ch ^ (rr & 7)) << 4)));
+        *reinterpret_cast<uint4 *>(dst + rr * stride + 8 * ch) = u;
+    }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }

@@ -187,43 +187,9 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         } else {
             tc_fence_after();
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const uint32_t stage = sb + w * TILE + quarter * (32 * D * 2);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t ov[32];
-                if (nt[w] > 0) {
-                    tc_ld32(to + 32 * i, ov);
-                    tc_wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t u[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        u[k] = inv == 0.f ? 0u
-                                          : pack_bf16(__uint_as_float(ov[8 * e + 2 * k]) * inv,
-                                                      __uint_as_float(ov[8 * e + 2 * k + 1]) * inv);
-                    const int ch = 4 * i + e;  // 16-byte piece of the row, swizzled by the row
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(stage + lane * (D * 2) +
-                                                                                   ((ch ^ (lane & 7)) << 4)),
-                                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                                 : "memory");
-                }
-            }
-            __syncwarp();
-            constexpr int PER = D * 2 / 16, ROWS = 32 / PER;  // pieces of a row, rows of one warp access
             const int first = r0 + w * AT + 32 * quarter;
-#pragma unroll
-            for (int i = 0; i < 32 / ROWS; ++i) {
-                const int rr = i * ROWS + lane / PER, ch = lane % PER;
-                if (first + rr >= sq.lq) continue;
-                uint32_t u[4];
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                             : "r"(stage + rr * (D * 2) + ((ch ^ (rr & 7)) << 4)));
-                *reinterpret_cast<uint4 *>(p.o + ((static_cast<int64_t>(sq.q0) + first + rr) * p.H + h) * D + 8 * ch) =
-                    make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            store_rows<D>(to, nt[w] > 0, inv, sb + w * TILE + quarter * (32 * D * 2), lane, sq.lq - first,
+                          p.o + ((static_cast<int64_t>(sq.q0) + first) * p.H + h) * D, static_cast<int64_t>(p.H) * D);
             if (row < sq.lq) {
                 const int64_t at = p.seq.cu_q ? static_cast<int64_t>(h) * p.seq.T + sq.q0 + row
                                               : (static_cast<int64_t>(n) * p.H + h) * p.seq.T + row;
@@ -251,7 +217,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     }
                     mbar_expect_tx(full0 + 8 * s, TILE);
                     for (int c = 0; c < HALVES; ++c)
-                        tma_load_3d(sb + S::RING + s * TILE + c * kHalfBytes, m, 64 * c, hk, sq.k0 + j * AT, full0 + 8 * s);
+                        tma_load_3d(sb + S::RING + s * TILE + c * kHalfBytes, m, 64 * c, hk, sq.k0 + j * AT,
+                                    full0 + 8 * s);
                     ++issued;
                     return true;
                 };
@@ -262,7 +229,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     ok = ok && load_kv(&mv, 0);
                     for (int j = 1; j < nmax && ok && !*abort_flag; ++j) ok = load_kv(&mk, j) && load_kv(&mv, j);
                     if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
-                        for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
+                        for (int i = max(0, issued - NST); i < issued; ++i)
+                            mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
                         for (int w = 0; w < 2; ++w)
                             if (nt[w]) mbar_wait(qfull0 + 8 * w, 0);
                     }
@@ -300,7 +268,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     const uint64_t b = vd + (rv % NST) * (TILE >> 4);
 #pragma unroll
                     for (int ks = 0; ks < AT / 16; ++ks)
-                        tc_mma_ts_warp(tmem + TM_O + D * w, tmem + 128 * w + 8 * ks, b + kstep_mn(ks), id_o, j > 0 || ks > 0);
+                        tc_mma_ts_warp(tmem + TM_O + D * w, tmem + 128 * w + 8 * ks, b + kstep_mn(ks), id_o,
+                                       j > 0 || ks > 0);
                     if (j + 1 < nt[w]) {
                         if (!wait(full0 + 8 * (rk % NST), (rk / NST) & 1)) break;
                         score(w, rk);

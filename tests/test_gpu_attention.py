@@ -50,8 +50,11 @@ def formula(q, k, v, scale, dout=None):
         delta = (do * o).sum(-1, keepdim=True)
         dp = do @ vv.transpose(1, 2)
         ds = p * (dp - delta) * scale
-        # what an error of delta (o is rounded to bf16) and of ds and p (rounded to bf16) is weighted with
-        ds_w = ds.abs() + p * scale * (do.abs() * o.abs()).sum(-1, keepdim=True)
+        # what ds is off by, in half steps: its own rounding, that of delta (from an o that is off by half a step of
+        # itself and of sum p |v|), and the fp32 sums of dp (2^-12 = 2^-4 half steps of the products)
+        o_w = p @ vv.abs()
+        ds_w = ds.abs() + p * scale * ((do.abs() * (o.abs() + o_w)).sum(-1, keepdim=True) +
+                                       2.0 ** -4 * (do.abs() @ vv.abs().transpose(1, 2)))
         share = lambda x: x.view(HKV, G, m, D).sum(1).transpose(0, 1)  # noqa: E731
         out.update(dq=(ds @ kk).transpose(0, 1), dq_w=(ds_w @ kk.abs()).transpose(0, 1),
                    dk=share(ds.transpose(1, 2) @ qq), dk_w=share(ds_w.transpose(1, 2) @ qq.abs()),
@@ -116,3 +119,35 @@ def test_forward_matches_the_formula(B, T, Tk, H, HKV, D, lens, klens):
     torch.cuda.synchronize()
     assert kda.device_error() == 0
     check_forward(q, k, v, o, lse, lens, klens)
+
+
+def check_backward(q, k, v, dout, grads, lens=None, klens=None, scale=None):
+    B, T, H, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    for b, a, n, c, m in sequences(B, T, k.shape[1], lens, klens):
+        if n == 0 or m == 0:
+            continue
+        f = formula(q[b, a:a + n], k[b, c:c + m], v[b, c:c + m], scale, dout[b, a:a + n])
+        for name, g, x, e in (("dq", grads[0], a, a + n), ("dk", grads[1], c, c + m), ("dv", grads[2], c, c + m)):
+            tol = (HALF + FP32) * f[name + "_w"] + HALF * f[name].abs() + 1e-30
+            ratio = ((g[b, x:e].double() - f[name]).abs() / tol).max()
+            assert ratio <= 1, (name, a, n, m, float(ratio))
+
+
+@pytest.mark.parametrize("B,T,Tk,H,HKV,D,lens,klens", CASES)
+def test_backward_matches_the_formula(B, T, Tk, H, HKV, D, lens, klens):
+    q, k, v = heads(1, B, T, H, D), heads(2, B, Tk, HKV, D), heads(3, B, Tk, HKV, D)
+    dout = heads(4, B, T, H, D, gain=0.0)
+    cu = None if lens is None else cu_of(lens)
+    cu_k = None if klens is None else cu_of(klens)
+    o, lse = kda.attention_forward(q, k, v, cu, cu_k)
+    grads = kda.attention_backward(q, k, v, o, lse, dout, cu, cu_k)
+    torch.cuda.synchronize()
+    assert kda.device_error() == 0
+    check_backward(q, k, v, dout, grads, lens, klens)
+    # rows without a counterpart have no gradient
+    for b, a, n, c, m in sequences(B, T, Tk, lens, klens):
+        if m == 0:
+            assert (grads[0][b, a:a + n] == 0).all()
+        if n == 0:
+            assert (grads[1][b, c:c + m] == 0).all() and (grads[2][b, c:c + m] == 0).all()
