@@ -426,6 +426,73 @@ kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const v
                                     int D, float scale, void *dq, void *dk, void *dv, void *workspace,
                                     size_t workspace_bytes, void *stream);
 
+/*
+ * The paged 8-bit key/value cache of the full-attention layers.  A cache holds
+ * num_blocks blocks of block_size (16, 32, 64 or 128) tokens: block b at
+ * cache + b * block_stride bytes, [HKV, block_size, D] codes, e4m3 or int8
+ * (-127..127), and one fp32 scale per (block, head), [num_blocks, HKV]; a value
+ * is code * scale.  Token p of a request lives in slot
+ *   block_table[row][p / block_size] * block_size + p % block_size.
+ *
+ * kda_cache_plan: block tables and slot maps on the device, from the lengths
+ * alone, so a captured step needs no host round trip.  Row b holds
+ * context_lens[b] tokens and gets new_lens[b] more (negative lengths count as
+ * zero).  The blocks it lacks are taken from the front of free_blocks, row by
+ * row, and written into its table row behind those it has:
+ *   block_table  int32 [B, table_width], rows table_stride elements apart, in/out
+ *   cu_seqlens   int32 [B + 1] out: the new tokens' row offsets
+ *   seq_lens     int32 [B] out: context_lens + new_lens
+ *   slot_map     int32 [num_tokens] out: each new token's slot, packed as
+ *                cu_seqlens says, -1 behind the last one (num_tokens is the
+ *                caller's bound on their number)
+ *   used         int32 [1] out: blocks taken
+ * If free_blocks, the table's width or num_tokens do not suffice, the tokens
+ * that miss a block get slot -1, table entries that miss one get -1, and bit 5
+ * (32) of the device error word is set.  B <= 16384.
+ *
+ * kda_cache_append: rounds rows of k and v (bf16 [T, HKV, D], strided rows) to
+ * codes in the slots of slot_map (-1: skipped).  The scale of a (block, head) is
+ * the smallest power of two that the tokens stored in it fit (their largest
+ * magnitude within 448 or 127 codes; infinities saturate and do not count, NaN
+ * becomes e4m3's NaN or int8's 0), and at least 2^-100.  Where the first of them does not
+ * open the block, the scale is never smaller than it was, and when it grows, the
+ * tokens before are rounded again.  Slots are unique; the tokens of one block
+ * stand beside one another in ascending order.  Slots past the cache are
+ * skipped and set bit 4 (16) of the device error word.
+ * k_cache and v_cache may interleave in one allocation.
+ */
+#define KDA_CACHE_E4M3 0
+#define KDA_CACHE_INT8 1
+kda_status_t kda_cache_plan(const int32_t *context_lens, const int32_t *new_lens, int B, int32_t *block_table,
+                            int64_t table_stride, int table_width, const int32_t *free_blocks, int num_free,
+                            int block_size, int32_t *cu_seqlens, int32_t *seq_lens, int32_t *slot_map, int num_tokens,
+                            int32_t *used, void *stream);
+kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride, void *k_cache,
+                              void *v_cache, int64_t block_stride, float *k_scale, float *v_scale, int code_type,
+                              int num_blocks, int block_size, const int32_t *slot_map, int T, int HKV, int D,
+                              void *stream);
+
+/*
+ * One-token attention over that cache: query row b sees the seq_lens[b] tokens
+ * of its block_table row (its own among them, once appended).
+ *   q    bf16, row b at q + b * q_row_stride: [H, D], 16-byte aligned, stride a
+ *        multiple of 8; query head h reads key/value head h / (H / HKV)
+ *   o    bf16 [B, H, D] out;  lse  fp32 [B, H] out (natural logarithm)
+ *   workspace  16-byte aligned, kda_attention_decode_workspace_size(...) bytes;
+ *        overlaps nothing else; calls that may run at the same time need their own
+ * A row of length 0 (or less) gets o = 0 and lse = -inf.  Tokens whose block is out of
+ * range do not count, a length past the table is cut off at it, and either sets
+ * bit 4 (16) of the device error word.  What a block holds behind the last token
+ * does not matter.  Value scales are positive; a block whose value scale is not
+ * counts as zeros.  The same bits on every run.
+ */
+size_t kda_attention_decode_workspace_size(int B, int H, int HKV, int D, int table_width, int block_size);
+kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride, const void *k_cache, const void *v_cache,
+                                  int64_t block_stride, const float *k_scale, const float *v_scale, int code_type,
+                                  int num_blocks, int block_size, const int32_t *block_table, int64_t table_stride,
+                                  int table_width, const int32_t *seq_lens, int B, int H, int HKV, int D, float scale,
+                                  void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,8 @@ EXPORTED = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill_forw
             "kda_prefill_state_bf16_workspace_size", "kda_prefill_forward_state_bf16",
             "kda_prefill_forward_save", "kda_prefill_backward_saved", "kda_prefill_forward_varlen",
             "kda_prefill_varlen_kernel_launches", "kda_attention_forward",
-            "kda_attention_backward_workspace_size", "kda_attention_backward")
+            "kda_attention_backward_workspace_size", "kda_attention_backward", "kda_cache_plan", "kda_cache_append",
+            "kda_attention_decode_workspace_size", "kda_attention_decode")
 
 
 class KdaError(RuntimeError):
@@ -99,6 +100,14 @@ def lib():
         L.kda_attention_backward_workspace_size.restype = Z
         L.kda_attention_backward.argtypes = [P, S, P, S, P, S, P, P, P, S, P, P] + [I] * 7 + [F, P, P, P, P, Z, P]
         L.kda_attention_backward.restype = I
+        L.kda_cache_plan.argtypes = [P, P, I, P, S, I, P, I, I, P, P, P, I, P, P]
+        L.kda_cache_plan.restype = I
+        L.kda_cache_append.argtypes = [P, S, P, S, P, P, S, P, P, I, I, I, P, I, I, I, P]
+        L.kda_cache_append.restype = I
+        L.kda_attention_decode_workspace_size.argtypes = [I] * 6
+        L.kda_attention_decode_workspace_size.restype = Z
+        L.kda_attention_decode.argtypes = [P, S, P, P, S, P, P, I, I, I, P, S, I, P, I, I, I, I, F, P, P, P, Z, P]
+        L.kda_attention_decode.restype = I
         _lib = L
         return L
 
@@ -555,3 +564,130 @@ def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None
                                           _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, dev))
     _check(rc, "kda_attention_backward")
     return dq, dk, dv
+
+
+def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num_tokens, *, stream=None):
+    """Block tables and slot maps of a paged cache from request lengths, on the GPU (CUDA).
+
+    context_lens, new_lens: int32 [B], tokens that each request holds and gets; block_table: int32 [B, width], updated
+    in place; free_blocks: int32 [F], taken from the front; num_tokens: the slot map's length, at least the sum of
+    new_lens.  Returns (cu_seqlens [B+1], seq_lens [B], slot_map [num_tokens], used [1]), all int32: the new tokens'
+    offsets, the lengths with them, each new token's slot (-1 behind the last), the number of blocks taken.
+    """
+    import torch
+    if block_table.dim() != 2 or block_table.shape[0] != context_lens.numel():
+        raise ValueError("block_table must be [B, width]")
+    B, width = block_table.shape
+    dev = context_lens.device
+    _need_all([("context_lens", context_lens, torch.int32, B, True), ("new_lens", new_lens, torch.int32, B, True),
+               ("block_table", block_table, torch.int32, None, False),
+               ("free_blocks", free_blocks, torch.int32, None, True)], dev)
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table must have compact rows")
+    # one allocation: cu_seqlens, seq_lens, used, slot_map
+    buf = torch.empty(2 * B + 2 + num_tokens, dtype=torch.int32, device=dev)
+    cu, lens, used, slots = buf[:B + 1], buf[B + 1:2 * B + 1], buf[2 * B + 1:2 * B + 2], buf[2 * B + 2:]
+    with _on(dev):
+        rc = lib().kda_cache_plan(_ptr(context_lens), _ptr(new_lens), B, _ptr(block_table),
+                                  block_table.stride(0) if B > 1 else width, width, _ptr(free_blocks),
+                                  free_blocks.numel(), block_size, _ptr(cu), _ptr(lens), _ptr(slots), num_tokens,
+                                  _ptr(used), _stream_ptr(stream, dev))
+    _check(rc, "kda_cache_plan")
+    return cu, lens, slots, used
+
+
+def _cache_inputs(k_cache, v_cache, k_scale, v_scale, device, more):
+    """Checks of a cache's tensors; returns (code type, num_blocks, HKV, block_size, D, block stride)."""
+    import torch
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks, HKV, block_size, D]")
+    if k_cache.dtype == torch.float8_e4m3fn:
+        code = 0
+    elif k_cache.dtype == torch.int8:
+        code = 1
+    else:
+        raise ValueError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
+    blocks, HKV, bs, D = k_cache.shape
+    _need_all([("k_cache", k_cache, k_cache.dtype, None, False), ("v_cache", v_cache, k_cache.dtype, None, False),
+               ("k_scale", k_scale, torch.float32, blocks * HKV, True),
+               ("v_scale", v_scale, torch.float32, blocks * HKV, True), *more], device)
+    stride = k_cache.stride(0) if blocks > 1 else HKV * bs * D
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t[0].is_contiguous() or (blocks > 1 and t.stride(0) != stride):
+            raise ValueError(f"{name} must be compact inside each block, with the same block stride as k_cache")
+    return code, blocks, HKV, bs, D, stride
+
+
+def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map, *, stream=None):
+    """Store the rows of k and v (bf16 [T,HKV,D]) in a paged 8-bit cache, in place (CUDA).
+
+    k_cache, v_cache: torch.float8_e4m3fn or torch.int8 [num_blocks,HKV,block_size,D], compact inside a block;
+    k_scale, v_scale: fp32 [num_blocks,HKV]; slot_map: int32 [T], -1 = skipped (see ``cache_plan``).  The scale of a
+    (block, head) is the smallest power of two that its tokens fit; it grows, and the block's earlier tokens are rounded
+    again, when later ones need it.
+    """
+    import torch
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [T,HKV,D]")
+    T, HKV, D = k.shape
+    dev = k.device
+    code, blocks, hkv, bs, d, stride = _cache_inputs(
+        k_cache, v_cache, k_scale, v_scale, dev,
+        [("k", k, torch.bfloat16, None, False), ("v", v, torch.bfloat16, None, False),
+         ("slot_map", slot_map, torch.int32, T, True)])
+    if (hkv, d) != (HKV, D):
+        raise ValueError("k and v must have the cache's heads")
+    with _on(dev):
+        rc = lib().kda_cache_append(_ptr(k), _row_stride("k", k[None]), _ptr(v), _row_stride("v", v[None]),
+                                    _ptr(k_cache), _ptr(v_cache), stride, _ptr(k_scale), _ptr(v_scale), code, blocks,
+                                    bs, _ptr(slot_map), T, HKV, D, _stream_ptr(stream, dev))
+    _check(rc, "kda_cache_append")
+
+
+def attention_decode_workspace_size(B, H, HKV, D, table_width, block_size) -> int:
+    return int(lib().kda_attention_decode_workspace_size(B, H, HKV, D, table_width, block_size))
+
+
+def attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *, scale=None, o=None, lse=None,
+                     workspace=None, stream=None):
+    """One-token attention over a paged 8-bit cache (CUDA); returns (o [B,H,D] bf16, lse [B,H] fp32).
+
+    q: bf16 [B,H,D], H a multiple of the cache's HKV, rows compact but they may be strided; the cache as in
+    ``cache_append``; block_table: int32 [B,width]; seq_lens: int32 [B], the tokens that row b sees (0: o = 0 and
+    lse = -inf).  scale: D^-0.5 when not given.
+    """
+    import torch
+    if q.dim() != 3 or block_table.dim() != 2 or block_table.shape[0] != q.shape[0]:
+        raise ValueError("q must be [B,H,D] and block_table [B,width]")
+    B, H, D = q.shape
+    width = block_table.shape[1]
+    dev = q.device
+    code, blocks, HKV, bs, d, stride = _cache_inputs(
+        k_cache, v_cache, k_scale, v_scale, dev,
+        [("q", q, torch.bfloat16, None, False), ("block_table", block_table, torch.int32, None, False),
+         ("seq_lens", seq_lens, torch.int32, B, True)])
+    if d != D:
+        raise ValueError("q must have the cache's head dimension")
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table must have compact rows")
+    if o is None:
+        o = torch.empty(B, H, D, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("o", o, torch.bfloat16, B * H * D, dev)
+    if lse is None:
+        lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, torch.float32, B * H, dev)
+    if workspace is None:
+        workspace = torch.empty(attention_decode_workspace_size(B, H, HKV, D, width, bs), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _need("workspace", workspace, torch.uint8, None, dev)
+    with _on(dev):
+        rc = lib().kda_attention_decode(_ptr(q), _row_stride("q", q[None]), _ptr(k_cache), _ptr(v_cache), stride,
+                                        _ptr(k_scale), _ptr(v_scale), code, blocks, bs, _ptr(block_table),
+                                        block_table.stride(0) if B > 1 else width, width, _ptr(seq_lens), B, H, HKV,
+                                        D, D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(workspace),
+                                        workspace.numel(), _stream_ptr(stream, dev))
+    _check(rc, "kda_attention_decode")
+    return o, lse

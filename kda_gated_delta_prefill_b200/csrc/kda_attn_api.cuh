@@ -2,7 +2,9 @@
 // include/kda_prefill.h): host-side argument checks, tensor maps, launches.
 #pragma once
 #include "kda_attn_backward.cuh"
+#include "kda_attn_decode.cuh"
 #include "kda_attn_forward.cuh"
+#include "kda_cache.cuh"
 
 namespace {
 
@@ -213,4 +215,276 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
                           kda_attn_dq_kernel<128>, AttnDqSmem<128>::TOTAL)
                     : run(kda_attn_stats_kernel<64>, kda_attn_dkv_kernel<64>, AttnDkvSmem<64>::TOTAL,
                           kda_attn_dq_kernel<64>, AttnDqSmem<64>::TOTAL);
+}
+
+// ---------------------------------------------------------------------------------------------- the 8-bit cache
+namespace {
+
+// log2 of a cache's block size, or -1.
+int block_shift(int block_size)
+{
+    return block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : block_size == 128 ? 7 : -1;
+}
+
+kda_status_t cache_dims(int code_type, int num_blocks, int block_size, int HKV, int D, int64_t block_stride)
+{
+    if (num_blocks <= 0 || HKV <= 0 || block_size <= 0) return KDA_ERR_INVALID_ARG;
+    if ((code_type != KDA_CACHE_E4M3 && code_type != KDA_CACHE_INT8) || block_shift(block_size) < 0 ||
+        (D != 64 && D != 128))
+        return KDA_ERR_UNSUPPORTED;
+    const int64_t block = static_cast<int64_t>(HKV) * block_size * D;
+    if (block_stride < block) return KDA_ERR_INVALID_ARG;
+    // slots and the rows of a block are int32
+    if (static_cast<int64_t>(num_blocks) * block_size > INT_MAX || block > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    if (block_stride % 16 || block_stride >= (1ll << 39)) return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+
+// The codes as a 3D map: D bytes, the rows of a block, the blocks; a box is `rows` rows of one block.
+bool cache_map(CUtensorMap *m, const void *base, int D, int block_rows, int num_blocks, int64_t block_stride, int rows)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(block_rows),
+                          static_cast<cuuint64_t>(num_blocks)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(block_stride)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" kda_status_t kda_cache_plan(const int32_t *context_lens, const int32_t *new_lens, int B,
+                                       int32_t *block_table, int64_t table_stride, int table_width,
+                                       const int32_t *free_blocks, int num_free, int block_size, int32_t *cu_seqlens,
+                                       int32_t *seq_lens, int32_t *slot_map, int num_tokens, int32_t *used,
+                                       void *stream)
+{
+    if (B <= 0 || table_width <= 0 || num_free < 0 || num_tokens < 0) return KDA_ERR_INVALID_ARG;
+    const int shift = block_shift(block_size);
+    if (shift < 0 || B > kda::kPlanMaxRows) return KDA_ERR_UNSUPPORTED;
+    if (table_stride < table_width) return KDA_ERR_INVALID_ARG;
+    if (!context_lens || !new_lens || !block_table || (num_free && !free_blocks) || !cu_seqlens || !seq_lens ||
+        (num_tokens && !slot_map) || !used)
+        return KDA_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(context_lens), static_cast<const void *>(new_lens),
+                          static_cast<const void *>(block_table), static_cast<const void *>(free_blocks),
+                          static_cast<const void *>(cu_seqlens), static_cast<const void *>(seq_lens),
+                          static_cast<const void *>(slot_map), static_cast<const void *>(used)})
+        if (!aligned(p, 4)) return KDA_ERR_MISALIGNED;
+    const size_t nb = static_cast<size_t>(B) * 4;
+    const Range out[] = {{block_table, span(B, table_stride, table_width, 4)}, {cu_seqlens, nb + 4}, {seq_lens, nb},
+                         {slot_map, static_cast<size_t>(num_tokens) * 4}, {used, 4}};
+    const Range in[] = {{context_lens, nb}, {new_lens, nb}, {free_blocks, static_cast<size_t>(num_free) * 4}};
+    if (outputs_overlap(out, in)) return KDA_ERR_INVALID_ARG;
+    DeviceInfo info;
+    if (device_info(info) != cudaSuccess) return KDA_ERR_CUDA;
+    using namespace kda;
+    const CachePlanParams p{context_lens, new_lens, block_table, free_blocks, cu_seqlens, seq_lens,  slot_map, used,
+                            table_stride, B,        table_width, num_free,    num_tokens, shift,     info.err};
+    // enough CTAs for two tokens a thread, or a warp per 4 rows, up to one CTA per SM
+    const int64_t want = std::max<int64_t>((num_tokens + 2ll * kPlanThreads - 1) / (2 * kPlanThreads), (B + 63) / 64);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, info.sms)));
+    const int smem = (2 * B + 1) * 4;
+    if (cudaFuncSetAttribute(kda_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    kda_cache_plan_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                                         void *k_cache, void *v_cache, int64_t block_stride, float *k_scale,
+                                         float *v_scale, int code_type, int num_blocks, int block_size,
+                                         const int32_t *slot_map, int T, int HKV, int D, void *stream)
+{
+    if (T < 0) return KDA_ERR_INVALID_ARG;
+    kda_status_t st = cache_dims(code_type, num_blocks, block_size, HKV, D, block_stride);
+    if (st != KDA_OK) return st;
+    if (T == 0) return KDA_OK;
+    const int64_t w = static_cast<int64_t>(HKV) * D;
+    if ((st = check_rows(k, T, k_row_stride, w)) != KDA_OK || (st = check_rows(v, T, v_row_stride, w)) != KDA_OK)
+        return st;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !slot_map) return KDA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(slot_map, 4))
+        return KDA_ERR_MISALIGNED;
+    const size_t pool = span(num_blocks, block_stride, w * block_size, 1), ns = static_cast<size_t>(num_blocks) * HKV * 4;
+    // k_cache and v_cache may interleave (one pool of [block][k, v]), but not at the same place
+    const int64_t apart = static_cast<const char *>(v_cache) - static_cast<const char *>(k_cache);
+    const int64_t block = w * block_size, gap = ((apart % block_stride) + block_stride) % block_stride;
+    if (overlaps(k_cache, pool, v_cache, pool) && (gap < block || gap > block_stride - block)) return KDA_ERR_INVALID_ARG;
+    const Range caches[] = {{k_cache, pool}, {v_cache, pool}};
+    const Range out[] = {{k_scale, ns}, {v_scale, ns}};
+    const Range in[] = {{k, span(T, k_row_stride, w, 2)}, {v, span(T, v_row_stride, w, 2)},
+                        {slot_map, static_cast<size_t>(T) * 4}};
+    if (outputs_overlap(out, in)) return KDA_ERR_INVALID_ARG;
+    for (const Range &c : caches) {
+        for (const Range &r : in)
+            if (overlaps(c.p, c.n, r.p, r.n)) return KDA_ERR_INVALID_ARG;
+        for (const Range &r : out)
+            if (overlaps(c.p, c.n, r.p, r.n)) return KDA_ERR_INVALID_ARG;
+    }
+    DeviceInfo info;
+    if (device_info(info) != cudaSuccess) return KDA_ERR_CUDA;
+    using namespace kda;
+    CacheAppendParams p{};
+    p.x[0] = static_cast<const __nv_bfloat16 *>(k);
+    p.x[1] = static_cast<const __nv_bfloat16 *>(v);
+    p.stride[0] = k_row_stride;
+    p.stride[1] = v_row_stride;
+    p.cache[0] = static_cast<uint8_t *>(k_cache);
+    p.cache[1] = static_cast<uint8_t *>(v_cache);
+    p.block_stride = block_stride;
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.slots = slot_map;
+    p.T = T;
+    p.HKV = HKV;
+    p.num_blocks = num_blocks;
+    p.err = info.err;
+    // windows as small as leaves four waves of CTAs (8 of them fit an SM)
+    const int per = 8 / (block_size / 16);
+    const int64_t groups = (2ll * HKV + per - 1) / per;
+    p.window = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(1, T * groups / (32ll * info.sms))));
+    const int64_t grid = (T + p.window - 1ll) / p.window * groups;
+    if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto fp8, auto d) {
+        constexpr bool F = decltype(fp8)::value;
+        constexpr int DD = decltype(d)::value;
+        const int g = static_cast<int>(grid);
+        if (block_size == 16) kda_cache_append_kernel<F, DD, 16><<<g, kAppendThreads, 0, s>>>(p);
+        else if (block_size == 32) kda_cache_append_kernel<F, DD, 32><<<g, kAppendThreads, 0, s>>>(p);
+        else if (block_size == 64) kda_cache_append_kernel<F, DD, 64><<<g, kAppendThreads, 0, s>>>(p);
+        else kda_cache_append_kernel<F, DD, 128><<<g, kAppendThreads, 0, s>>>(p);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (code_type == KDA_CACHE_E4M3) D == 128 ? go(std::true_type{}, D128{}) : go(std::true_type{}, D64{});
+    else D == 128 ? go(std::false_type{}, D128{}) : go(std::false_type{}, D64{});
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+namespace {
+
+// Query heads of a unit, and the most CTAs that a decode step uses, whatever the device.
+int decode_heads(int H, int HKV) { return H / HKV <= 8 ? 8 : 16; }
+int64_t decode_ctas(int B, int H, int HKV, int table_width, int block_size)
+{
+    const int64_t hb = decode_heads(H, HKV), chunks = (H / HKV + hb - 1) / hb;
+    const int64_t tiles = (static_cast<int64_t>(table_width) * block_size + kda::kAdTile - 1) / kda::kAdTile;
+    const int64_t row = HKV * chunks;  // each factor may be near 2^31
+    return tiles >= kda::kAdMaxCtas || row >= kda::kAdMaxCtas ? kda::kAdMaxCtas
+                                                              : std::min<int64_t>(kda::kAdMaxCtas, B * (tiles * row));
+}
+size_t decode_part_bytes(int64_t ctas, int H, int HKV, int D)
+{
+    return round_up(static_cast<size_t>(ctas) * 2 * decode_heads(H, HKV) * (D + 2) * 4, kAlign);
+}
+
+}  // namespace
+
+extern "C" size_t kda_attention_decode_workspace_size(int B, int H, int HKV, int D, int table_width, int block_size)
+{
+    if (B <= 0 || H <= 0 || HKV <= 0 || H % HKV || (D != 64 && D != 128) || table_width <= 0 ||
+        block_shift(block_size) < 0)
+        return 0;
+    const int64_t ctas = decode_ctas(B, H, HKV, table_width, block_size);
+    return decode_part_bytes(ctas, H, HKV, D) + round_up(static_cast<size_t>(ctas) * sizeof(int2), kAlign);
+}
+
+extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride, const void *k_cache,
+                                             const void *v_cache, int64_t block_stride, const float *k_scale,
+                                             const float *v_scale, int code_type, int num_blocks, int block_size,
+                                             const int32_t *block_table, int64_t table_stride, int table_width,
+                                             const int32_t *seq_lens, int B, int H, int HKV, int D, float scale,
+                                             void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (B < 0 || H <= 0 || HKV <= 0 || H % HKV != 0 || table_width <= 0 || !(scale > 0.f) || scale > 3e38f)
+        return KDA_ERR_INVALID_ARG;
+    kda_status_t st = cache_dims(code_type, num_blocks, block_size, HKV, D, block_stride);
+    if (st != KDA_OK) return st;
+    if (B == 0) return KDA_OK;
+    if (static_cast<int64_t>(B) * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    const int64_t wq = static_cast<int64_t>(H) * D;
+    if ((st = check_rows(q, B, q_row_stride, wq)) != KDA_OK) return st;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !o || !lse ||
+        table_stride < table_width)
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = kda_attention_decode_workspace_size(B, H, HKV, D, table_width, block_size);
+    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(workspace, 16))
+        return KDA_ERR_MISALIGNED;
+    const size_t pool = span(num_blocks, block_stride, static_cast<int64_t>(HKV) * block_size * D, 1);
+    const size_t ns = static_cast<size_t>(num_blocks) * HKV * 4;
+    const Range out[] = {{o, span(B, wq, wq, 2)}, {lse, static_cast<size_t>(B) * H * 4}, {workspace, need}};
+    const Range in[] = {{q, span(B, q_row_stride, wq, 2)}, {k_cache, pool}, {v_cache, pool}, {k_scale, ns},
+                        {v_scale, ns}, {block_table, span(B, table_stride, table_width, 4)},
+                        {seq_lens, static_cast<size_t>(B) * 4}};
+    if (outputs_overlap(out, in)) return KDA_ERR_INVALID_ARG;
+    DeviceInfo info;
+    if (device_info(info) != cudaSuccess) return KDA_ERR_CUDA;
+    using namespace kda;
+    const int hb = decode_heads(H, HKV);
+    const int64_t ctas = decode_ctas(B, H, HKV, table_width, block_size);
+    AttnDecodeParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_row_stride;
+    p.kscale = k_scale;
+    p.vscale = v_scale;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.lens = seq_lens;
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.part = static_cast<float *>(workspace);
+    p.shared_unit = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + decode_part_bytes(ctas, H, HKV, D));
+    p.err = info.err;
+    p.B = B;
+    p.H = H;
+    p.HKV = HKV;
+    p.chunks = (H / HKV + hb - 1) / hb;
+    p.width = table_width;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * kLog2e;
+    const int rows = std::min(block_size, kAdTile), shift = block_shift(block_size);
+    CUtensorMap mk, mv;
+    if (!cache_map(&mk, k_cache, D, HKV * block_size, num_blocks, block_stride, rows) ||
+        !cache_map(&mv, v_cache, D, HKV * block_size, num_blocks, block_stride, rows))
+        return KDA_ERR_CUDA;
+    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(info.sms) * kAdCtasPerSm));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto fp8, auto d, auto nt) {
+        constexpr bool F = decltype(fp8)::value;
+        constexpr int DD = decltype(d)::value, N = decltype(nt)::value;
+        auto kern = kda_attn_decode_kernel<F, DD, N>;
+        constexpr int smem = AttnDecodeSmem<DD, N>::TOTAL;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        kern<<<grid, kAdThreads, smem, s>>>(p, mk, mv, shift);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        // the join waits for the pieces on the device (griddepcontrol.wait), so its launch overlaps the step
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(32 * hb);
+        cfg.stream = s;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kda_attn_decode_join_kernel<DD>, p, hb) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    using N1 = std::integral_constant<int, 1>;
+    using N2 = std::integral_constant<int, 2>;
+    auto by_heads = [&](auto fp8, auto d) { return hb == 8 ? go(fp8, d, N1{}) : go(fp8, d, N2{}); };
+    auto by_dim = [&](auto fp8) { return D == 128 ? by_heads(fp8, D128{}) : by_heads(fp8, D64{}); };
+    return code_type == KDA_CACHE_E4M3 ? by_dim(std::true_type{}) : by_dim(std::false_type{});
 }

@@ -1,0 +1,526 @@
+// kda_attn_decode.cuh -- one-token attention over the paged 8-bit cache.
+//
+//   s_j = scale q . (ks_b code_k[j]),  o = sum_j softmax(s)_j vs_b code_v[j],  lse = log sum_j exp(s_j)
+// with ks_b and vs_b the scales of token j's block and head.  Bound by reading the codes once: 2 D bytes per token and
+// key/value head.
+//
+// The work is cut evenly over the CTAs, whatever the lengths: the tiles of 64 tokens of all (row, key/value head)
+// units stand in one line of W, and CTA c of G <= W takes tiles [c W / G, (c + 1) W / G) of it.  A unit inside one CTA is
+// finished there; of a unit that several CTAs share, each leaves its maximum, sum and accumulator, and a second, dependent
+// launch joins them in the order of the CTAs.
+//
+// In a CTA, one warp requests the tiles' pages by TMA through a ring; four warps take 16 tokens of a tile each, with a
+// running softmax of their own, and join at the end of the unit.  All query heads of a group share one pass over the
+// codes, as columns of mma.sync: S^T = K Q^T and O^T += V^T P^T, whose M dimension is the tokens, or the head
+// dimension.  The codes become fp16 exactly in registers (both code types fit), a query row becomes fp16 after a power
+// of two makes its largest element 1..2 (exact, but for elements 2^-14 smaller than it, which round at 2^-24 of it).
+// tcgen05 would want the codes in shared memory as fp16, and at 24 bytes per cycle and SM mma.sync is not what bounds.
+//
+// The value scale goes into the exponent: with t_j = s_j log2(e) + log2(vs_b), the weights p_j = 2^(t_j - M) are
+// what multiplies the codes and p_j / vs_b is what the softmax's sum adds.  M is a running reference of t, so a weight is
+// small only where its product with the codes is.  Weights are fp16 (11 bits), 2^12 at the reference and at most
+// 2^15, which keeps what is flushed below 2^-37 of the largest.
+#pragma once
+#include "kda_attn_common.cuh"
+#include "kda_cache.cuh"
+
+namespace kda {
+
+constexpr int kAdTile = 64, kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512, kAdCtasPerSm = 2;
+
+struct AttnDecodeParams {
+    const __nv_bfloat16 *q;  // row b at q + b * q_stride: [H, D]
+    int64_t q_stride;
+    const float *kscale, *vscale;  // [num_blocks, HKV]
+    const int32_t *table;          // [B, width], rows table_stride apart
+    int64_t table_stride;
+    const int32_t *lens;           // [B]
+    __nv_bfloat16 *o;              // [B, H, D]
+    float *lse;                    // [B, H]
+    float *part;                   // [G][2][HB][D + 2]: accumulator, reference, sum; HB heads of a unit
+    int2 *shared_unit;             // [G]: the unit that begins in CTA c and goes on behind it (or -1), CTAs behind
+    unsigned *err;
+    int B, H, HKV, chunks, width, num_blocks;  // chunks of HB query heads of a group
+    float scale_log2;
+};
+
+template <int D, int NT>
+struct AttnDecodeSmem {
+    static constexpr int HB = 8 * NT;                  // query heads of a unit
+    static constexpr int HALF = kAdTile * D;           // K or V codes of a tile
+    static constexpr int NST = (NT == 1 ? 5 : 4) * (128 / D);
+    static constexpr int JOIN = NST * 2 * HALF;        // fp32 [4 warps][HB][D]
+    static constexpr int STATS = JOIN + kAdWarps * HB * D * 4;   // fp32 [4 warps][HB][2]
+    static constexpr int META = STATS + kAdWarps * HB * 2 * 4;   // float4 [NST][4 slices]
+    static constexpr int SCAN = META + NST * kAdWarps * 16;      // int64 [5 warps], start {b, tile}
+    static constexpr int BAR = SCAN + 64 + 16;
+    static constexpr int ABORT = BAR + 2 * NST * 8;
+    static constexpr int TOTAL = ABORT + 8;
+};
+
+// Where CTA c's share of W tiles begins.
+__device__ __forceinline__ int64_t share(int64_t W, int c, int G) { return W * c / G; }
+
+__device__ __forceinline__ void mma_f16_2(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    const uint32_t a[4] = {a0, a1, a2, a3};
+    mma_f16(d, a, b0, b1);
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+// Codes to fp16 pairs: bytes 0 and 1 of w into lo, 2 and 3 into hi.
+template <bool FP8>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (FP8) {
+        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // byte u = code + 128 as the low bits of fp16 1024 + u; minus 1152
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const uint32_t off = 0x64806480u;  // 1152
+        asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(lo) : "r"(a), "r"(off));
+        asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(b), "r"(off));
+    }
+}
+
+template <bool FP8, int D, int NT>
+__global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
+    kda_attn_decode_kernel(const AttnDecodeParams p, const __grid_constant__ CUtensorMap mk,
+                           const __grid_constant__ CUtensorMap mv, const int shift)
+{
+    using S = AttnDecodeSmem<D, NT>;
+    constexpr int NST = S::NST, HB = S::HB, HALF = S::HALF, KS = D / 16, MT = D / 16;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x;
+    const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
+    const int bs = 1 << shift;
+    const int cap = static_cast<int>(min(static_cast<int64_t>(p.width) << shift, static_cast<int64_t>(INT_MAX) - 64));
+    const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST;
+    float4 *meta = reinterpret_cast<float4 *>(sm + S::META);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
+    auto len_of = [&](int b) { return min(max(p.lens[b], 0), cap); };
+    auto tiles_of = [&](int b) { return (len_of(b) + kAdTile - 1) / kAdTile; };
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, kAdWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    // ---------------- W, and the row in which this CTA's share begins ----------------
+    int64_t *scan = reinterpret_cast<int64_t *>(sm + S::SCAN);
+    const int per = (p.B + kAdThreads - 1) / kAdThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+    int64_t inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += x;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, W = 0;
+    for (int w = 0; w < kAdThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        W += scan[w];
+    }
+    W *= units_row;
+    const int G = static_cast<int>(min(W, static_cast<int64_t>(gridDim.x)));  // CTAs with work: a tile each at least
+    const int64_t g0 = c < G ? share(W, c, G) : 0, g1 = c < G ? share(W, c + 1, G) : 0;
+    // rows without tokens: zeros (every CTA some of them); too long for the table: an error
+    for (int b = c; b < p.B; b += gridDim.x) {
+        if (p.lens[b] > cap && tid == 0) atomicOr(p.err, ERR_BLOCK_ID);
+        if (len_of(b) > 0) continue;
+        for (int i = tid; i < p.H * D / 2; i += kAdThreads)
+            reinterpret_cast<uint32_t *>(p.o + static_cast<int64_t>(b) * p.H * D)[i] = 0u;
+        for (int i = tid; i < p.H; i += kAdThreads) p.lse[static_cast<int64_t>(b) * p.H + i] = -INFINITY;
+    }
+    int *start = reinterpret_cast<int *>(sm + S::SCAN + 64);
+    if (g0 < g1 && g0 >= before * units_row && g0 < (before + mine) * units_row) {
+        int64_t at = before;
+        int b = b0;
+        for (; g0 >= (at + tiles_of(b)) * units_row; ++b) at += tiles_of(b);
+        start[0] = b;
+        *reinterpret_cast<int64_t *>(start + 2) = g0 - at * units_row;
+    }
+    if (tid == 0) p.shared_unit[c] = make_int2(-1, 0);
+    __syncthreads();
+    if (g0 >= g1) return;
+
+    // the share as pieces: row, unit in the row, tiles [t0, t1) of the unit's n
+    int b = start[0], n = tiles_of(b);
+    int64_t inrow = *reinterpret_cast<int64_t *>(start + 2);
+    int u = static_cast<int>(inrow / n), t0 = static_cast<int>(inrow - static_cast<int64_t>(u) * n);
+    int64_t left = g1 - g0;
+    auto next = [&](int t1) {  // behind tile t1 - 1 of this unit
+        left -= t1 - t0;
+        t0 = 0;
+        if (left > 0 && ++u == units_row) {
+            u = 0;
+            do ++b;
+            while ((n = tiles_of(b)) == 0);
+        }
+    };
+
+    if (warp == kAdWarps) {
+        // ---------------- loads: lane = tile (of 8) * 4 + slice of 16 tokens ----------------
+        const int slices_page = bs / 16, rows = min(bs, kAdTile);   // slices of a page; rows of one copy
+        int it = 0;
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(n), t0 + left));
+            const int len = len_of(b), hk = u / p.chunks;
+            auto ids = [&](int t) {  // the block of this lane's slice, tiles t .. t + 7
+                const int tok = (t + (lane >> 2)) * kAdTile + 16 * (lane & 3);
+                if (t + (lane >> 2) >= t1 || tok >= len) return -2;
+                const int id = p.table[b * p.table_stride + (tok >> shift)];
+                return id >= 0 && id < p.num_blocks ? id : -1;
+            };
+            int id = ids(t0);
+            for (int t = t0; t < t1 && ok; t += 8) {
+                const int far = ids(t + 8);
+                float ks = 0.f, vs = 0.f;
+                if (id >= 0) {
+                    ks = p.kscale[static_cast<int64_t>(id) * p.HKV + hk];
+                    vs = p.vscale[static_cast<int64_t>(id) * p.HKV + hk];
+                }
+                if (__any_sync(0xffffffffu, id == -1) && lane == 0) atomicOr(p.err, ERR_BLOCK_ID);
+                // a slice that counts: scale of the scores, log2 and inverse of the value scale.  All of a block's
+                // values are zero where its scale is: any scale will do then
+                const float v1 = vs > 0.f ? vs : 1.f;
+                const float4 m = make_float4(ks, log2f(v1), 1.f / v1, id >= 0 ? (vs > 0.f ? 1.f : 2.f) : 0.f);
+                // the lane that copies: the first slice of a page, or of a tile inside a longer page
+                const bool copies = id >= 0 && (slices_page >= 4 ? (lane & 3) == 0 : (lane & 3) % slices_page == 0);
+                const uint32_t who = __ballot_sync(0xffffffffu, copies);
+                for (int k = 0; k < 8 && t + k < t1; ++k, ++it) {
+                    const int st = it % NST;
+                    if (it >= NST) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * st, ((it / NST) - 1) & 1));
+                        if (!ok || *abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if ((lane >> 2) == k) meta[st * kAdWarps + (lane & 3)] = m;
+                    __syncwarp();
+                    const uint32_t mine4 = (who >> (4 * k)) & 15u;
+                    if (lane == 0) mbar_expect_tx(full0 + 8 * st, __popc(mine4) * 2 * rows * D);
+                    __syncwarp();
+                    if ((lane >> 2) == k && copies) {
+                        const int tok = (t + k) * kAdTile + 16 * (lane & 3);
+                        const uint32_t dst = sb + st * 2 * HALF + 16 * (lane & 3) * D;
+                        const int row = hk * bs + (tok & (bs - 1));
+                        tma_load_3d(dst, &mk, 0, row, id, full0 + 8 * st);
+                        tma_load_3d(dst + HALF, &mv, 0, row, id, full0 + 8 * st);
+                    }
+                }
+                id = far;
+            }
+            next(t1);
+        }
+        if (!ok) {  // let the copies in flight land before the CTA leaves
+            if (lane == 0) {
+                atomicOr(p.err, ERR_PIPE_EMPTY_WAIT);
+                *abort_flag = 1;
+            }
+            for (int i = max(0, it - NST); i < it; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
+        }
+        return;
+    }
+
+    // ---------------- arithmetic: warp w takes slice w of every tile ----------------
+    const int r = lane >> 2, cc = lane & 3;
+    float *join = reinterpret_cast<float *>(sm + S::JOIN), *stats = reinterpret_cast<float *>(sm + S::STATS);
+    int it = 0;
+    bool ok = true;
+    while (left > 0) {
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(n), t0 + left));
+        const int len = len_of(b), hk = u / p.chunks, hc = u % p.chunks;
+        const int heads = min(HB, group - hc * HB), head0 = hk * group + hc * HB;
+        // query rows as B operands: column r (head), the dims that this lane's K words hold
+        uint32_t qf[NT][KS][2];
+        float f0[NT], f1[NT];  // score factors of heads 2 cc and 2 cc + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int hd = 8 * nt + r;
+            const __nv_bfloat16 *src = p.q + b * p.q_stride + static_cast<int64_t>(head0 + hd) * D + cc * (D / 4);
+            uint4 raw[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                raw[i] = hd < heads ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t top = 0;
+            auto word = [&](int k) {
+                const uint4 &v = raw[k >> 2];
+                return (k & 3) == 0 ? v.x : (k & 3) == 1 ? v.y : (k & 3) == 2 ? v.z : v.w;
+            };
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                const uint32_t a = word(k) & 0x7fff7fffu;
+                top = max(top, max(a & 0xffffu, a >> 16));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max(static_cast<int>(top >> 7), 1), 253);  // exponent of the largest element
+            const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                qf[nt][k >> 1][k & 1] = pack_f16(bf16lo(word(k)) * down, bf16hi(word(k)) * down);
+            const float f = up * p.scale_log2;
+            f0[nt] = __shfl_sync(0xffffffffu, f, 8 * cc);
+            f1[nt] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
+        }
+        float acc[NT][MT][4], M0[NT], M1[NT], l0[NT], l1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            M0[nt] = M1[nt] = -INFINITY;
+            l0[nt] = l1[nt] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+        }
+        // after a wait that ran out the warp only keeps the others company at the barriers
+        for (int t = t0; t < t1 && ok; ++t, ++it) {
+            const int st = it % NST;
+            ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * st, (it / NST) & 1));
+            if (!ok) break;
+            const float4 m = meta[st * kAdWarps + warp];
+            const int have = len - t * kAdTile - 16 * warp;  // tokens of the slice
+            if (have > 0 && m.w != 0.f) {
+                const uint8_t *kt = sm + st * 2 * HALF, *vt = kt + HALF;
+                const int row = 16 * warp + r;
+                uint32_t kw[2][D / 16];  // token r and r + 8: the words of this lane's D / 4 dims
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rw = row + 8 * i;
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j) {
+                        const int ch = D == 128 ? ((2 * cc + j) ^ (rw & 7)) : (cc ^ ((rw >> 1) & 3));
+                        const uint4 v = *reinterpret_cast<const uint4 *>(kt + rw * D + 16 * ch);
+                        kw[i][4 * j] = v.x;
+                        kw[i][4 * j + 1] = v.y;
+                        kw[i][4 * j + 2] = v.z;
+                        kw[i][4 * j + 3] = v.w;
+                    }
+                }
+                float s[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16<FP8>(kw[0][k], a0, a2);
+                    codes_to_f16<FP8>(kw[1][k], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_2(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+                }
+                // V words: tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9; dims of chunk r
+                uint32_t vw[4][D / 32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 2 * cc + (i & 1) + 8 * (i >> 1), rw = 16 * warp + tok;
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vt + rw * D + 16 * (r ^ (rw & 7)));
+                        vw[i][0] = v.x;
+                        vw[i][1] = v.y;
+                        vw[i][2] = v.z;
+                        vw[i][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(
+                            vt + rw * D + 16 * ((r >> 1) ^ ((rw >> 1) & 3)) + 8 * (r & 1));
+                        vw[i][0] = v.x;
+                        vw[i][1] = v.y;
+                    }
+                    // codes behind the last token, and of a block without a scale, may be anything
+                    if (tok >= have || m.w == 2.f)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) vw[i][k] = 0u;
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float a = f0[nt] * m.x, bq = f1[nt] * m.x;
+                    float x0 = fmaf(s[nt][0], a, m.y), x1 = fmaf(s[nt][1], bq, m.y);
+                    float x2 = fmaf(s[nt][2], a, m.y), x3 = fmaf(s[nt][3], bq, m.y);
+                    if (r >= have) x0 = x1 = -INFINITY;
+                    if (r + 8 >= have) x2 = x3 = -INFINITY;
+                    float h0 = fmaxf(x0, x2), h1 = fmaxf(x1, x3);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                        h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, off));
+                        h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, off));
+                    }
+                    const bool g0_ = h0 > M0[nt] + 3.f, g1_ = h1 > M1[nt] + 3.f;
+                    if (__any_sync(0xffffffffu, g0_ || g1_)) {
+                        const float n0 = g0_ ? h0 : M0[nt], n1 = g1_ ? h1 : M1[nt];
+                        const float al0 = g0_ ? ex2(M0[nt] - n0) : 1.f, al1 = g1_ ? ex2(M1[nt] - n1) : 1.f;
+                        M0[nt] = n0;
+                        M1[nt] = n1;
+                        l0[nt] *= al0;
+                        l1[nt] *= al1;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            acc[nt][i][0] *= al0;
+                            acc[nt][i][1] *= al1;
+                            acc[nt][i][2] *= al0;
+                            acc[nt][i][3] *= al1;
+                        }
+                    }
+                    const float e0 = 12.f - M0[nt], e1 = 12.f - M1[nt];
+                    x0 = ex2(x0 + e0);
+                    x1 = ex2(x1 + e1);
+                    x2 = ex2(x2 + e0);
+                    x3 = ex2(x3 + e1);
+                    l0[nt] = fmaf(x0 + x2, m.z, l0[nt]);
+                    l1[nt] = fmaf(x1 + x3, m.z, l1[nt]);
+                    pb[nt][0] = movmatrix(pack_f16(x0, x1));
+                    pb[nt][1] = movmatrix(pack_f16(x2, x3));
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    // bytes of two tokens side by side: A operand pairs along the tokens
+                    uint32_t a[2][4];  // dims 4 w + {0, 1} and {2, 3} of the chunk: a0 a1 a2 a3
+#pragma unroll
+                    for (int pr = 0; pr < 2; ++pr) {
+                        const uint32_t lo = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x5140);
+                        const uint32_t hi = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x7362);
+                        codes_to_f16<FP8>(lo, a[0][2 * pr], a[0][2 * pr + 1]);
+                        codes_to_f16<FP8>(hi, a[1][2 * pr], a[1][2 * pr + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + i], a[i], pb[nt][0], pb[nt][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * st);
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, ERR_PIPE_FULL_WAIT);
+            *abort_flag = 1;
+        }
+        // ---------------- join the four warps ----------------
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                l0[nt] += __shfl_xor_sync(0xffffffffu, l0[nt], off);
+                l1[nt] += __shfl_xor_sync(0xffffffffu, l1[nt], off);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float *dst = join + (warp * HB + 8 * nt + 2 * cc + hh) * D + r * (D / 8);
+#pragma unroll
+                for (int i = 0; i < MT; i += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * i) = make_float4(
+                        acc[nt][i][hh], acc[nt][i][2 + hh], acc[nt][i + 1][hh], acc[nt][i + 1][2 + hh]);
+            }
+            if (r == 0) {
+                float *st = stats + (warp * HB + 8 * nt + 2 * cc) * 2;
+                st[0] = M0[nt];
+                st[1] = l0[nt];
+                st[2] = M1[nt];
+                st[3] = l1[nt];
+            }
+        }
+        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
+        const bool whole = t0 == 0 && t1 == n;
+        float *part = p.part + (static_cast<int64_t>(2 * c + (t0 > 0 ? 0 : 1)) * HB) * (D + 2);
+        for (int i = tid; i < heads * (D / 4); i += 32 * kAdWarps) {
+            const int hd = i / (D / 4), d = 4 * (i % (D / 4));
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAdWarps; ++w) M = fmaxf(M, stats[(w * HB + hd) * 2]);
+            float l = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAdWarps; ++w) {
+                const float Mw = stats[(w * HB + hd) * 2], lw = stats[(w * HB + hd) * 2 + 1];
+                const float f = Mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2(Mw - M);
+                const float4 v = *reinterpret_cast<const float4 *>(join + (w * HB + hd) * D + d);
+                l = fmaf(lw, f, l);
+                a = make_float4(fmaf(v.x, f, a.x), fmaf(v.y, f, a.y), fmaf(v.z, f, a.z), fmaf(v.w, f, a.w));
+            }
+            if (whole) {
+                const int64_t at = static_cast<int64_t>(b) * p.H + head0 + hd;
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // no token counted (blocks out of range): zeros
+                *reinterpret_cast<uint2 *>(p.o + at * D + d) =
+                    l == 0.f ? make_uint2(0u, 0u)
+                             : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+                if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
+            } else {
+                float *dst = part + hd * (D + 2);
+                dst[d] = a.x;
+                dst[d + 1] = a.y;
+                dst[d + 2] = a.z;
+                dst[d + 3] = a.w;
+                if (d == 0) {
+                    dst[D] = M;
+                    dst[D + 1] = l;
+                }
+            }
+        }
+        if (t0 == 0 && t1 < n && tid == 0) {  // it goes on in the CTAs behind
+            const int64_t end = g1 + (n - t1) - 1;  // its last tile: in the CTA k with share(k) <= end < share(k + 1)
+            int k = static_cast<int>(end * G / W);
+            while (share(W, k + 1, G) <= end) ++k;
+            while (share(W, k, G) > end) --k;
+            p.shared_unit[c] = make_int2(b * units_row + u, k - c);
+        }
+        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
+        next(t1);
+    }
+}
+
+// Joins the pieces of a unit that began in CTA c: a warp per query head.
+template <int D>
+__global__ void __launch_bounds__(512) kda_attn_decode_join_kernel(const AttnDecodeParams p, const int HB)
+{
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int c = blockIdx.x, hd = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int2 su = p.shared_unit[c];
+    if (su.x < 0) return;
+    const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
+    const int b = su.x / units_row, u = su.x % units_row, hk = u / p.chunks, hc = u % p.chunks;
+    if (hd >= min(HB, group - hc * HB)) return;
+    // the piece of CTA c is its last one, those of the CTAs behind their first
+    auto piece = [&](int k) {
+        return p.part + (static_cast<int64_t>(2 * (c + k) + (k == 0 ? 1 : 0)) * HB + hd) * (D + 2);
+    };
+    float M = -INFINITY;
+    for (int k = lane; k <= su.y; k += 32) M = fmaxf(M, piece(k)[D]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float l = 0.f, a[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) a[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k <= su.y; ++k) {
+        const float *src = piece(k);
+        const float Mk = src[D], lk = src[D + 1];
+        const float f = Mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : ex2(Mk - M);
+        l = fmaf(lk, f, l);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) a[i] = fmaf(src[32 * i + lane], f, a[i]);
+    }
+    const int64_t at = static_cast<int64_t>(b) * p.H + hk * group + hc * HB + hd;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        p.o[at * D + 32 * i + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : a[i] / l);
+    if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
+}
+
+}  // namespace kda
