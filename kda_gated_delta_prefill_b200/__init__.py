@@ -16,6 +16,7 @@ cu_seqlens [N+1] int32 or None (then B must be 1).  Returns o
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -133,6 +134,15 @@ def _need_all(checks, device=None, *, host=False):
     """The library reads and writes raw pointers, so a tensor of another dtype or size would let its kernels run
     past the buffer.  ``checks``: (name, tensor or None, dtype, element count or None, contiguous); first every
     dtype and size, then placement (``device``, or host memory) and layout."""
+    if device is not None and device.type == "cuda":  # one cheap pass when nothing is wrong
+        index = device.index
+        for _, t, dtype, numel, contiguous in checks:
+            if t is not None and (t.dtype is not dtype or t.get_device() != index
+                                  or (numel is not None and t.numel() != numel)
+                                  or (contiguous and not t.is_contiguous())):
+                break
+        else:
+            return
     checks = [c for c in checks if c[1] is not None]
     for name, t, dtype, numel, _ in checks:
         if t.dtype != dtype:
@@ -467,43 +477,71 @@ def forward_noalloc(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, o=
     return o, final_state
 
 
-def _row_stride(name, t):
-    """Elements between the rows of a [B,T,heads,D] tensor whose rows are compact and evenly spaced."""
-    B, T, heads, D = t.shape
-    sb, st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (heads > 1 and sh != D):
+# ---------------------------------------------------------------------------------------------- softmax attention
+# These calls take a few microseconds on the GPU for short requests, so their host side is kept as short: pointers
+# as plain integers, the device switched only where it is not the current one.
+def _call(name, dev, stream, *args):
+    """Call a C entry whose last argument is the stream, on the tensors' device."""
+    import torch
+    if torch.cuda.current_device() != dev.index:
+        with _on(dev):
+            return _call(name, dev, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    rc = getattr(_lib or lib(), name)(*args, s)
+    if rc != 0:
+        raise KdaError(rc, name)
+
+
+def _scale(scale, D):
+    return (max(D, 1) ** -0.5) if scale is None else scale
+
+
+def _row_stride(name, shape, strides):
+    """Elements between the rows of a [B,T,heads,D] (or [T,heads,D]) tensor, which are compact and evenly spaced."""
+    D, heads = shape[-1], shape[-2]
+    if (strides[-1] != 1 and D > 1) or (strides[-2] != D and heads > 1):
         raise ValueError(f"{name} must have compact rows")
+    T = shape[-3]
+    B = shape[0] if len(shape) == 4 else 1
     if T > 1:
-        if B > 1 and sb != T * st:
+        st = strides[-3]
+        if B > 1 and strides[0] != T * st:
             raise ValueError(f"{name} must have evenly spaced rows")
         return st
-    return sb if B > 1 else heads * D
+    return strides[0] if B > 1 else heads * D
 
 
 def _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, more=()):
-    """Checks of attention over whole prompts; returns (B, T, Tk, H, HKV, D, num_seqs, device, cu_seqlens_k)."""
+    """Checks of attention over whole prompts; returns the C calls' leading arguments (pointers and row strides of q, k
+    and v), (cu_seqlens, cu_seqlens_k, num_seqs, B, T, Tk, H, HKV, D), and the device."""
     import torch
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B,T,H,D], k and v [B,Tk,HKV,D]")
-    B, T, H, D = q.shape
-    Tk, HKV = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+    qs, ks = q.shape, k.shape
+    B, T, H, D = qs
+    Bk, Tk, HKV, Dk = ks
+    if Bk != B or Dk != D or v.shape != ks:
         raise ValueError("q must be [B,T,H,D], k and v [B,Tk,HKV,D]")
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens
-        if T != Tk and cu_seqlens is not None:
-            raise ValueError("keys of another length than the queries need cu_seqlens_k")
-    elif cu_seqlens is None:
-        raise ValueError("cu_seqlens_k needs cu_seqlens")
     num_seqs = 0
-    if cu_seqlens is not None:
+    if cu_seqlens is None:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+    else:
         num_seqs = cu_seqlens.numel() - 1
         if num_seqs < 1:
             raise ValueError("cu_seqlens must hold at least 2 elements")
-    _need_all([("q", q, torch.bfloat16, None, False), ("k", k, torch.bfloat16, None, False),
-               ("v", v, torch.bfloat16, None, False), ("cu_seqlens", cu_seqlens, torch.int32, None, True),
-               ("cu_seqlens_k", cu_seqlens_k, torch.int32, num_seqs + 1, True), *more], q.device)
-    return B, T, Tk, H, HKV, D, num_seqs, q.device, cu_seqlens_k
+        if cu_seqlens_k is None:
+            if T != Tk:
+                raise ValueError("keys of another length than the queries need cu_seqlens_k")
+            cu_seqlens_k = cu_seqlens
+    bf16 = torch.bfloat16
+    dev = q.device
+    _need_all([("q", q, bf16, None, False), ("k", k, bf16, None, False), ("v", v, bf16, None, False),
+               ("cu_seqlens", cu_seqlens, torch.int32, None, True),
+               ("cu_seqlens_k", cu_seqlens_k, torch.int32, num_seqs + 1, True), *more], dev)
+    cu, cu_k = (None, None) if cu_seqlens is None else (cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr())
+    return ((q.data_ptr(), _row_stride("q", qs, q.stride()), k.data_ptr(), _row_stride("k", ks, k.stride()),
+             v.data_ptr(), _row_stride("v", ks, v.stride())), (cu, cu_k, num_seqs, B, T, Tk, H, HKV, D), dev)
 
 
 def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, o=None, lse=None, stream=None):
@@ -516,7 +554,8 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
     scale: D^-0.5 when not given.  lse is the natural logarithm of the row's sum of exponentials.
     """
     import torch
-    B, T, Tk, H, HKV, D, num_seqs, dev, cu_k = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
+    rows, dims, dev = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
+    B, T, H, D = q.shape
     if o is None:
         o = torch.empty(B, T, H, D, dtype=torch.bfloat16, device=dev)
     else:
@@ -525,12 +564,8 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
         lse = torch.empty(B, H, T, dtype=torch.float32, device=dev)
     else:
         _need("lse", lse, torch.float32, B * H * T, dev)
-    with _on(dev):
-        rc = lib().kda_attention_forward(_ptr(q), _row_stride("q", q), _ptr(k), _row_stride("k", k), _ptr(v),
-                                         _row_stride("v", v), _ptr(cu_seqlens), _ptr(cu_k), num_seqs, B, T, Tk, H,
-                                         HKV, D, D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse),
-                                         _stream_ptr(stream, dev))
-    _check(rc, "kda_attention_forward")
+    _call("kda_attention_forward", dev, stream, *rows, *dims, _scale(scale, D), o.data_ptr(),
+          lse.data_ptr())
     return o, lse
 
 
@@ -546,24 +581,29 @@ def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None
     key/value head.  dout's rows may be strided like q's.  Rows of no sequence are not written.
     """
     import torch
-    B, T, Tk, H, HKV, D, num_seqs, dev, cu_k = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
-    if dout.dim() != 4 or dout.shape != q.shape:
+    B, T, H, D = q.shape
+    rows, dims, dev = _attention_inputs(
+        q, k, v, cu_seqlens, cu_seqlens_k,
+        (("o", o, torch.bfloat16, B * T * H * D, True), ("lse", lse, torch.float32, B * H * T, True),
+         ("dout", dout, torch.bfloat16, None, False), ("workspace", workspace, torch.uint8, None, True)))
+    if dout.shape != q.shape:
         raise ValueError("dout must be [B,T,H,D]")
-    _need_all([("o", o, torch.bfloat16, B * T * H * D, True), ("lse", lse, torch.float32, B * H * T, True),
-               ("dout", dout, torch.bfloat16, None, False), ("workspace", workspace, torch.uint8, None, True)], dev)
     dq = torch.empty(B, T, H, D, dtype=torch.bfloat16, device=dev)
-    dk = torch.empty(B, Tk, HKV, D, dtype=torch.bfloat16, device=dev)
-    dv = torch.empty(B, Tk, HKV, D, dtype=torch.bfloat16, device=dev)
+    dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    dv = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     if workspace is None:
-        workspace = torch.empty(attention_backward_workspace_size(B, T, H, num_seqs), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib().kda_attention_backward(_ptr(q), _row_stride("q", q), _ptr(k), _row_stride("k", k), _ptr(v),
-                                          _row_stride("v", v), _ptr(o), _ptr(lse), _ptr(dout),
-                                          _row_stride("dout", dout), _ptr(cu_seqlens), _ptr(cu_k), num_seqs, B, T, Tk,
-                                          H, HKV, D, D ** -0.5 if scale is None else scale, _ptr(dq), _ptr(dk),
-                                          _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, dev))
-    _check(rc, "kda_attention_backward")
+        workspace = torch.empty(attention_backward_workspace_size(B, T, H, dims[2]), dtype=torch.uint8, device=dev)
+    _call("kda_attention_backward", dev, stream, *rows, o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+          _row_stride("dout", dout.shape, dout.stride()), *dims, _scale(scale, D), dq.data_ptr(),
+          dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
+
+
+def _table_stride(block_table, B, width):
+    sb, sw = block_table.stride()
+    if sw != 1 and width > 1:
+        raise ValueError("block_table must have compact rows")
+    return sb if B > 1 else width
 
 
 def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num_tokens, *, stream=None):
@@ -572,78 +612,85 @@ def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num
     context_lens, new_lens: int32 [B], tokens that each request holds and gets; block_table: int32 [B, width], updated
     in place; free_blocks: int32 [F], taken from the front; num_tokens: the slot map's length, at least the sum of
     new_lens.  Returns (cu_seqlens [B+1], seq_lens [B], slot_map [num_tokens], used [1]), all int32: the new tokens'
-    offsets, the lengths with them, each new token's slot (-1 behind the last), the number of blocks taken.
+    offsets, the lengths with them, each new token's slot (-1 behind the last), the number of blocks taken.  What does
+    not fit gets -1 and sets bit 5 of ``device_error``.
     """
     import torch
-    if block_table.dim() != 2 or block_table.shape[0] != context_lens.numel():
+    B = context_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, width]")
-    B, width = block_table.shape
+    if num_tokens < 0:
+        raise ValueError("num_tokens must not be negative")
+    width = block_table.shape[1]
     dev = context_lens.device
-    _need_all([("context_lens", context_lens, torch.int32, B, True), ("new_lens", new_lens, torch.int32, B, True),
-               ("block_table", block_table, torch.int32, None, False),
-               ("free_blocks", free_blocks, torch.int32, None, True)], dev)
-    if width > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table must have compact rows")
-    # one allocation: cu_seqlens, seq_lens, used, slot_map
-    buf = torch.empty(2 * B + 2 + num_tokens, dtype=torch.int32, device=dev)
-    cu, lens, used, slots = buf[:B + 1], buf[B + 1:2 * B + 1], buf[2 * B + 1:2 * B + 2], buf[2 * B + 2:]
-    with _on(dev):
-        rc = lib().kda_cache_plan(_ptr(context_lens), _ptr(new_lens), B, _ptr(block_table),
-                                  block_table.stride(0) if B > 1 else width, width, _ptr(free_blocks),
-                                  free_blocks.numel(), block_size, _ptr(cu), _ptr(lens), _ptr(slots), num_tokens,
-                                  _ptr(used), _stream_ptr(stream, dev))
-    _check(rc, "kda_cache_plan")
+    i32 = torch.int32
+    _need_all((("context_lens", context_lens, i32, B, True), ("new_lens", new_lens, i32, B, True),
+               ("block_table", block_table, i32, None, False), ("free_blocks", free_blocks, i32, None, True)), dev)
+    table_stride = _table_stride(block_table, B, width)
+    buf = torch.empty(2 * B + 2 + num_tokens, dtype=i32, device=dev)
+    slots, cu, lens, used = torch.unsafe_split_with_sizes(buf, (num_tokens, B + 1, B, 1))
+    at = buf.data_ptr()
+    small = at + 4 * num_tokens
+    _call("kda_cache_plan", dev, stream, context_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
+          table_stride, width, free_blocks.data_ptr(), free_blocks.numel(), block_size, small,
+          small + 4 * (B + 1), at, num_tokens, small + 4 * (2 * B + 1))
     return cu, lens, slots, used
 
 
 def _cache_inputs(k_cache, v_cache, k_scale, v_scale, device, more):
     """Checks of a cache's tensors; returns (code type, num_blocks, HKV, block_size, D, block stride)."""
     import torch
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, HKV, block_size, D]")
-    if k_cache.dtype == torch.float8_e4m3fn:
+    dtype = k_cache.dtype
+    if dtype is torch.float8_e4m3fn:
         code = 0
-    elif k_cache.dtype == torch.int8:
+    elif dtype is torch.int8:
         code = 1
     else:
-        raise ValueError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
-    blocks, HKV, bs, D = k_cache.shape
-    _need_all([("k_cache", k_cache, k_cache.dtype, None, False), ("v_cache", v_cache, k_cache.dtype, None, False),
+        raise ValueError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {dtype}")
+    blocks, HKV, bs, D = shape
+    _need_all((("k_cache", k_cache, dtype, None, False), ("v_cache", v_cache, dtype, None, False),
                ("k_scale", k_scale, torch.float32, blocks * HKV, True),
-               ("v_scale", v_scale, torch.float32, blocks * HKV, True), *more], device)
-    stride = k_cache.stride(0) if blocks > 1 else HKV * bs * D
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t[0].is_contiguous() or (blocks > 1 and t.stride(0) != stride):
-            raise ValueError(f"{name} must be compact inside each block, with the same block stride as k_cache")
-    return code, blocks, HKV, bs, D, stride
+               ("v_scale", v_scale, torch.float32, blocks * HKV, True), *more), device)
+    strides = k_cache.stride()
+    inside = (bs * D, D, 1)
+    if strides != v_cache.stride() or strides[1:] != inside:  # (the stride of an axis of length 1 says nothing)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if any(t.shape[i + 1] > 1 and t.stride(i + 1) != inside[i] for i in range(3)) or \
+                    (blocks > 1 and t.stride(0) != strides[0]):
+                raise ValueError(f"{name} must be compact inside each block, with k_cache's block stride")
+    return code, blocks, HKV, bs, D, strides[0] if blocks > 1 else HKV * bs * D
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map, *, stream=None):
     """Store the rows of k and v (bf16 [T,HKV,D]) in a paged 8-bit cache, in place (CUDA).
 
     k_cache, v_cache: torch.float8_e4m3fn or torch.int8 [num_blocks,HKV,block_size,D], compact inside a block;
-    k_scale, v_scale: fp32 [num_blocks,HKV]; slot_map: int32 [T], -1 = skipped (see ``cache_plan``).  The scale of a
-    (block, head) is the smallest power of two that its tokens fit; it grows, and the block's earlier tokens are rounded
-    again, when later ones need it.
+    k_scale, v_scale: fp32 [num_blocks,HKV]; slot_map: int32 [T], -1 = skipped (see ``cache_plan``); slots are unique,
+    and the tokens of one block stand beside one another, in ascending order.  The scale of a (block, head) is the
+    smallest power of two that its tokens fit; it grows, and the block's earlier tokens are rounded again, when later ones
+    need it.
     """
     import torch
-    if k.dim() != 3 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be [T,HKV,D]")
-    T, HKV, D = k.shape
+    T, HKV, D = shape
     dev = k.device
     code, blocks, hkv, bs, d, stride = _cache_inputs(
         k_cache, v_cache, k_scale, v_scale, dev,
-        [("k", k, torch.bfloat16, None, False), ("v", v, torch.bfloat16, None, False),
-         ("slot_map", slot_map, torch.int32, T, True)])
-    if (hkv, d) != (HKV, D):
+        (("k", k, torch.bfloat16, None, False), ("v", v, torch.bfloat16, None, False),
+         ("slot_map", slot_map, torch.int32, T, True)))
+    if hkv != HKV or d != D:
         raise ValueError("k and v must have the cache's heads")
-    with _on(dev):
-        rc = lib().kda_cache_append(_ptr(k), _row_stride("k", k[None]), _ptr(v), _row_stride("v", v[None]),
-                                    _ptr(k_cache), _ptr(v_cache), stride, _ptr(k_scale), _ptr(v_scale), code, blocks,
-                                    bs, _ptr(slot_map), T, HKV, D, _stream_ptr(stream, dev))
-    _check(rc, "kda_cache_append")
+    _call("kda_cache_append", dev, stream, k.data_ptr(), _row_stride("k", shape, k.stride()), v.data_ptr(),
+          _row_stride("v", shape, v.stride()), k_cache.data_ptr(), v_cache.data_ptr(), stride, k_scale.data_ptr(),
+          v_scale.data_ptr(), code, blocks, bs, slot_map.data_ptr(), T, HKV, D)
 
 
+@functools.lru_cache(maxsize=256)
 def attention_decode_workspace_size(B, H, HKV, D, table_width, block_size) -> int:
     return int(lib().kda_attention_decode_workspace_size(B, H, HKV, D, table_width, block_size))
 
@@ -654,22 +701,22 @@ def attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
 
     q: bf16 [B,H,D], H a multiple of the cache's HKV, rows compact but they may be strided; the cache as in
     ``cache_append``; block_table: int32 [B,width]; seq_lens: int32 [B], the tokens that row b sees (0: o = 0 and
-    lse = -inf).  scale: D^-0.5 when not given.
+    lse = -inf).  scale: D^-0.5 when not given.  Blocks out of range do not count and set bit 4 of ``device_error``.
     """
     import torch
-    if q.dim() != 3 or block_table.dim() != 2 or block_table.shape[0] != q.shape[0]:
+    qs, ts = q.shape, block_table.shape
+    if len(qs) != 3 or len(ts) != 2 or ts[0] != qs[0]:
         raise ValueError("q must be [B,H,D] and block_table [B,width]")
-    B, H, D = q.shape
-    width = block_table.shape[1]
+    B, H, D = qs
+    width = ts[1]
     dev = q.device
     code, blocks, HKV, bs, d, stride = _cache_inputs(
         k_cache, v_cache, k_scale, v_scale, dev,
-        [("q", q, torch.bfloat16, None, False), ("block_table", block_table, torch.int32, None, False),
-         ("seq_lens", seq_lens, torch.int32, B, True)])
+        (("q", q, torch.bfloat16, None, False), ("block_table", block_table, torch.int32, None, False),
+         ("seq_lens", seq_lens, torch.int32, B, True)))
     if d != D:
         raise ValueError("q must have the cache's head dimension")
-    if width > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table must have compact rows")
+    table_stride = _table_stride(block_table, B, width)
     if o is None:
         o = torch.empty(B, H, D, dtype=torch.bfloat16, device=dev)
     else:
@@ -683,11 +730,8 @@ def attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
                                 device=dev)
     else:
         _need("workspace", workspace, torch.uint8, None, dev)
-    with _on(dev):
-        rc = lib().kda_attention_decode(_ptr(q), _row_stride("q", q[None]), _ptr(k_cache), _ptr(v_cache), stride,
-                                        _ptr(k_scale), _ptr(v_scale), code, blocks, bs, _ptr(block_table),
-                                        block_table.stride(0) if B > 1 else width, width, _ptr(seq_lens), B, H, HKV,
-                                        D, D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(workspace),
-                                        workspace.numel(), _stream_ptr(stream, dev))
-    _check(rc, "kda_attention_decode")
+    _call("kda_attention_decode", dev, stream, q.data_ptr(), _row_stride("q", qs, q.stride()), k_cache.data_ptr(),
+          v_cache.data_ptr(), stride, k_scale.data_ptr(), v_scale.data_ptr(), code, blocks, bs, block_table.data_ptr(),
+          table_stride, width, seq_lens.data_ptr(), B, H, HKV, D, _scale(scale, D), o.data_ptr(),
+          lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return o, lse

@@ -285,10 +285,10 @@ extern "C" kda_status_t kda_cache_plan(const int32_t *context_lens, const int32_
     using namespace kda;
     const CachePlanParams p{context_lens, new_lens, block_table, free_blocks, cu_seqlens, seq_lens,  slot_map, used,
                             table_stride, B,        table_width, num_free,    num_tokens, shift,     info.err};
-    // enough CTAs for two tokens a thread, or a warp per 4 rows, up to one CTA per SM
-    const int64_t want = std::max<int64_t>((num_tokens + 2ll * kPlanThreads - 1) / (2 * kPlanThreads), (B + 63) / 64);
+    // enough CTAs for four tokens a thread, or a warp per 4 rows, up to one CTA per SM
+    const int64_t want = std::max<int64_t>((num_tokens + 4ll * kPlanThreads - 1) / (4 * kPlanThreads), (B + 63) / 64);
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, info.sms)));
-    const int smem = (2 * B + 1) * 4;
+    const int smem = (3 * B + 1) * 4;
     if (cudaFuncSetAttribute(kda_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return KDA_ERR_CUDA;
     kda_cache_plan_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
@@ -345,21 +345,24 @@ extern "C" kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, co
     p.HKV = HKV;
     p.num_blocks = num_blocks;
     p.err = info.err;
-    // windows as small as leaves four waves of CTAs (8 of them fit an SM)
-    const int per = 8 / (block_size / 16);
-    const int64_t groups = (2ll * HKV + per - 1) / per;
-    p.window = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(1, T * groups / (32ll * info.sms))));
-    const int64_t grid = (T + p.window - 1ll) / p.window * groups;
+    // Windows as small as leaves four waves of CTAs (8 of them fit an SM): one token for a step of requests, a block for
+    // prompts.  256 single tokens (8 heads, blocks of 64): 5 us with one warp a unit, 11 with four; prompts of 97,000 tokens
+    // (blocks of 16, where both are the same) do not differ.
+    const int wpu = block_size / 16;
+    const int64_t wide = (2ll * HKV * wpu + 7) / 8;  // CTAs of a run with BS / 16 warps a unit
+    p.window = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(1, T * wide / (32ll * info.sms))));
+    const bool few = p.window == 1;
+    const int64_t grid = (T + p.window - 1ll) / p.window * (few ? (2ll * HKV + 7) / 8 : wide);
     if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto go = [&](auto fp8, auto d) {
         constexpr bool F = decltype(fp8)::value;
         constexpr int DD = decltype(d)::value;
-        const int g = static_cast<int>(grid);
-        if (block_size == 16) kda_cache_append_kernel<F, DD, 16><<<g, kAppendThreads, 0, s>>>(p);
-        else if (block_size == 32) kda_cache_append_kernel<F, DD, 32><<<g, kAppendThreads, 0, s>>>(p);
-        else if (block_size == 64) kda_cache_append_kernel<F, DD, 64><<<g, kAppendThreads, 0, s>>>(p);
-        else kda_cache_append_kernel<F, DD, 128><<<g, kAppendThreads, 0, s>>>(p);
+        auto run = [&](auto kern) { kern<<<static_cast<int>(grid), kAppendThreads, 0, s>>>(p); };
+        if (block_size == 16) run(kda_cache_append_kernel<F, DD, 16, 1>);
+        else if (block_size == 32) few ? run(kda_cache_append_kernel<F, DD, 32, 1>) : run(kda_cache_append_kernel<F, DD, 32, 2>);
+        else if (block_size == 64) few ? run(kda_cache_append_kernel<F, DD, 64, 1>) : run(kda_cache_append_kernel<F, DD, 64, 4>);
+        else few ? run(kda_cache_append_kernel<F, DD, 128, 1>) : run(kda_cache_append_kernel<F, DD, 128, 8>);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
@@ -471,14 +474,14 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
         // the join waits for the pieces on the device (griddepcontrol.wait), so its launch overlaps the step
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(32 * hb);
+        cfg.blockDim = dim3(kAdJoinThreads);
         cfg.stream = s;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kda_attn_decode_join_kernel<DD>, p, hb) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, kda_attn_decode_join_kernel<DD, N>, p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

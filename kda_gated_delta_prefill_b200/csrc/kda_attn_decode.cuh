@@ -37,7 +37,7 @@ struct AttnDecodeParams {
     const int32_t *lens;           // [B]
     __nv_bfloat16 *o;              // [B, H, D]
     float *lse;                    // [B, H]
-    float *part;                   // [G][2][HB][D + 2]: accumulator, reference, sum; HB heads of a unit
+    float *part;                   // [G][2] pieces: accumulators [HB][D], then reference and sum [HB][2]
     int2 *shared_unit;             // [G]: the unit that begins in CTA c and goes on behind it (or -1), CTAs behind
     unsigned *err;
     int B, H, HKV, chunks, width, num_blocks;  // chunks of HB query heads of a group
@@ -89,6 +89,17 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
         asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(lo) : "r"(a), "r"(off));
         asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(b), "r"(off));
     }
+}
+
+// Four dims of a head's result from its accumulator, reference and sum (0: no token counted).
+template <int D>
+__device__ __forceinline__ void store_attention(const AttnDecodeParams &p, int b, int h, int d, float4 a, float M, float l)
+{
+    const int64_t at = static_cast<int64_t>(b) * p.H + h;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(p.o + at * D + d) =
+        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
 }
 
 template <bool FP8, int D, int NT>
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
         }
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
         const bool whole = t0 == 0 && t1 == n;
-        float *part = p.part + (static_cast<int64_t>(2 * c + (t0 > 0 ? 0 : 1)) * HB) * (D + 2);
+        float *part = p.part + static_cast<int64_t>(2 * c + (t0 > 0 ? 0 : 1)) * (HB * (D + 2));
         for (int i = tid; i < heads * (D / 4); i += 32 * kAdWarps) {
             const int hd = i / (D / 4), d = 4 * (i % (D / 4));
             float M = -INFINITY;
@@ -455,22 +466,10 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
                 a = make_float4(fmaf(v.x, f, a.x), fmaf(v.y, f, a.y), fmaf(v.z, f, a.z), fmaf(v.w, f, a.w));
             }
             if (whole) {
-                const int64_t at = static_cast<int64_t>(b) * p.H + head0 + hd;
-                const float inv = l == 0.f ? 0.f : 1.f / l;  // no token counted (blocks out of range): zeros
-                *reinterpret_cast<uint2 *>(p.o + at * D + d) =
-                    l == 0.f ? make_uint2(0u, 0u)
-                             : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-                if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
+                store_attention<D>(p, b, head0 + hd, d, a, M, l);
             } else {
-                float *dst = part + hd * (D + 2);
-                dst[d] = a.x;
-                dst[d + 1] = a.y;
-                dst[d + 2] = a.z;
-                dst[d + 3] = a.w;
-                if (d == 0) {
-                    dst[D] = M;
-                    dst[D + 1] = l;
-                }
+                *reinterpret_cast<float4 *>(part + hd * D + d) = a;
+                if (d == 0) *reinterpret_cast<float2 *>(part + HB * D + 2 * hd) = make_float2(M, l);
             }
         }
         if (t0 == 0 && t1 < n && tid == 0) {  // it goes on in the CTAs behind
@@ -485,42 +484,56 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
     }
 }
 
-// Joins the pieces of a unit that began in CTA c: a warp per query head.
-template <int D>
-__global__ void __launch_bounds__(512) kda_attn_decode_join_kernel(const AttnDecodeParams p, const int HB)
+// Joins the pieces of a unit that began in CTA c, in their order: a thread per head and four dims.  Bound by the latency of
+// three dependent loads (which unit, the pieces' references, their accumulators).
+constexpr int kAdJoinThreads = 256;
+template <int D, int NT>
+__global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(const AttnDecodeParams p)
 {
+    constexpr int HB = 8 * NT, PIECE = HB * (D + 2);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int c = blockIdx.x, hd = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
     const int2 su = p.shared_unit[c];
     if (su.x < 0) return;
     const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
     const int b = su.x / units_row, u = su.x % units_row, hk = u / p.chunks, hc = u % p.chunks;
-    if (hd >= min(HB, group - hc * HB)) return;
+    const int heads = min(HB, group - hc * HB);
     // the piece of CTA c is its last one, those of the CTAs behind their first
-    auto piece = [&](int k) {
-        return p.part + (static_cast<int64_t>(2 * (c + k) + (k == 0 ? 1 : 0)) * HB + hd) * (D + 2);
-    };
-    float M = -INFINITY;
-    for (int k = lane; k <= su.y; k += 32) M = fmaxf(M, piece(k)[D]);
+    const float *first = p.part + (2ll * c + 1) * PIECE, *rest = p.part + 2ll * c * PIECE;
+    auto piece = [&](int k) { return k == 0 ? first : rest + 2ll * k * PIECE; };
+    for (int i = threadIdx.x; i < heads * (D / 4); i += kAdJoinThreads) {
+        const int hd = i / (D / 4), d = 4 * (i % (D / 4));
+        float M = -INFINITY, l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 <= su.y; k0 += 8) {  // eight pieces' loads in flight
+            float2 ml[8];
+            float4 v[8];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float l = 0.f, a[D / 32];
+            for (int k = 0; k < 8; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k <= su.y) {
+                    const float *src = piece(k0 + k);
+                    ml[k] = *reinterpret_cast<const float2 *>(src + HB * D + 2 * hd);
+                    v[k] = *reinterpret_cast<const float4 *>(src + hd * D + d);
+                }
+            }
+            float Mn = M;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) a[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k <= su.y; ++k) {
-        const float *src = piece(k);
-        const float Mk = src[D], lk = src[D + 1];
-        const float f = Mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : ex2(Mk - M);
-        l = fmaf(lk, f, l);
+            for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, ml[k].x);
+            const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
+            l *= f0;
+            a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) a[i] = fmaf(src[32 * i + lane], f, a[i]);
+            for (int k = 0; k < 8; ++k) {
+                const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - Mn);
+                l = fmaf(ml[k].y, f, l);
+                a = make_float4(fmaf(v[k].x, f, a.x), fmaf(v[k].y, f, a.y), fmaf(v[k].z, f, a.z), fmaf(v[k].w, f, a.w));
+            }
+            M = Mn;
+        }
+        store_attention<D>(p, b, hk * group + hc * HB + hd, d, a, M, l);
     }
-    const int64_t at = static_cast<int64_t>(b) * p.H + hk * group + hc * HB + hd;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        p.o[at * D + 32 * i + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : a[i] / l);
-    if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
 }
 
 }  // namespace kda

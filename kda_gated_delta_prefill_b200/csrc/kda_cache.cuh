@@ -30,7 +30,8 @@ constexpr int kPlanThreads = 512, kPlanMaxRows = 16384;
 __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const CachePlanParams p)
 {
     extern __shared__ int32_t plan_sm[];
-    int32_t *cu = plan_sm, *take = plan_sm + p.B + 1;  // [B + 1] tokens before row b, [B] blocks taken before it
+    // [B + 1] tokens before row b; [B] blocks taken before it; [B] tokens held
+    int32_t *cu = plan_sm, *take = cu + p.B + 1, *held = take + p.B;
     __shared__ int2 part[kPlanThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = 1 << p.shift, per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
         const int c = ctx(b), a = add(b);
         cu[b] = at.x;
         take[b] = at.y;
+        held[b] = c;
         if (blockIdx.x == 0) {
             p.cu_seqlens[b] = at.x;
             p.seq_lens[b] = c + a;
@@ -95,26 +97,43 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
             p.block_table[b * p.table_stride + k] = f < p.num_free ? p.free_blocks[f] : -1;
         }
     }
-    // the slot of each token; -1 behind the last one, and where there is no block
-    for (int t = blockIdx.x * kPlanThreads + tid; t < p.tokens; t += gridDim.x * kPlanThreads) {
-        int slot = -1;
+    // The slot of each token; -1 behind the last one, and where there is no block.  A thread takes four tokens: one search
+    // and one table entry, unless a row or a block ends among them.
+    int steps = 0;
+    while ((1 << steps) < p.B) ++steps;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0;
+    for (int t = 4 * (blockIdx.x * kPlanThreads + tid); t < p.tokens; t += 4 * gridDim.x * kPlanThreads) {
+        int slot[4] = {-1, -1, -1, -1};
         if (t < all.x) {
-            int lo = 0, hi = p.B;  // the last row that starts at or before t (rows without tokens start where the next does)
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            const int c = ctx(lo), pos = c + t - cu[lo], k = pos >> p.shift, have = blocks(c);
-            if (k < p.width) {
-                const int f = take[lo] + k - have;
-                const int id = k < have          ? p.block_table[lo * p.table_stride + k]
-                               : f < p.num_free  ? p.free_blocks[f]
-                                                 : -1;
-                if (id >= 0 && id <= (INT_MAX >> p.shift)) slot = (id << p.shift) + (pos & (bs - 1));
+            int row = 0;  // the last row that starts at or before t (rows without tokens start where the next does)
+            for (int w = 1 << steps >> 1; w > 0; w >>= 1)
+                if (row + w < p.B && cu[row + w] <= t) row += w;
+            auto place = [&](int r, int pos) {
+                const int k = pos >> p.shift;
+                if (k >= p.width) return -1;
+                const int have = blocks(held[r]), f = take[r] + k - have;
+                const int id = k < have ? p.block_table[r * p.table_stride + k]
+                               : f < p.num_free ? p.free_blocks[f]
+                                                : -1;
+                return id >= 0 && id <= (INT_MAX >> p.shift) ? (id << p.shift) + (pos & (bs - 1)) : -1;
+            };
+            const int pos = held[row] + t - cu[row];
+            if (t + 4 <= cu[row + 1] && (pos & (bs - 1)) + 4 <= bs) {
+                const int s0 = place(row, pos);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) slot[j] = s0 < 0 ? -1 : s0 + j;
+            } else {
+                for (int j = 0; j < 4 && t + j < all.x; ++j) {
+                    while (cu[row + 1] <= t + j) ++row;
+                    slot[j] = place(row, held[row] + t + j - cu[row]);
+                }
             }
         }
-        p.slot_map[t] = slot;
+        if (wide && t + 4 <= p.tokens) {
+            *reinterpret_cast<int4 *>(p.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+            for (int j = 0; j < 4 && t + j < p.tokens; ++j) p.slot_map[t + j] = slot[j];
+        }
     }
 }
 
@@ -146,6 +165,23 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
         return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
     }
 }
+// four finite bf16 values times a power of two -> four codes.  int8 rounds by adding 1.5 * 2^23: the sum's low byte is
+// the integer nearest the product (exact, at most 127), ties to even.
+template <bool FP8>
+__device__ __forceinline__ uint32_t encode4(uint2 x, float inv)
+{
+    const float2 a = unpack_bf16(x.x), b = unpack_bf16(x.y), i2 = make_float2(inv, inv);
+    if constexpr (!FP8) {
+        const float2 magic = make_float2(12582912.f, 12582912.f);
+        const float2 u = fma2(a, i2, magic), v = fma2(b, i2, magic);
+        const uint32_t lo = __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        const float2 u = mul2(a, i2), v = mul2(b, i2);
+        return encode4<FP8>(u.x, u.y, v.x, v.y);
+    }
+}
 // four codes -> four floats
 template <bool FP8>
 __device__ __forceinline__ float4 decode4(uint32_t w)
@@ -164,86 +200,126 @@ __device__ __forceinline__ float4 decode4(uint32_t w)
 }
 
 // A run is the tokens of one block that stand beside one another in the call; its first token leads it.  A CTA looks
-// at `window` tokens and, for each leader among them, stores the run's tokens of 8 / (BS / 16) (head, k or v) units:
-// BS / 16 warps a unit, 16 tokens a warp, held in registers between the maximum and the rounding, so every input byte
-// is read once.  Windows are one token where there are few tokens (each may lead its own block) and up to a block where
-// there are many (most of them follow a leader).  Bound by HBM for prompts (2 bytes in, 1 out per element), by latency
-// for one token per request.
-template <bool FP8, int D, int BS>
-__global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(const CacheAppendParams p)
+// at `window` tokens and, for each leader among them, stores the run's tokens of 8 / WPU (head, k or v) units, WPU
+// warps a unit, 16 tokens a warp at a time.  With many tokens windows are as long as a block (most tokens follow a
+// leader) and WPU = BS / 16: a warp's 16 tokens stay in registers between the maximum and the rounding, and every
+// input byte is read once.  With few tokens (each may lead its own block) a window is one token and WPU = 1, so
+// that no warp is without a token; a longer run is then read twice.  Bound by HBM for prompts (2 bytes in, 1 out per
+// element), by the latency of slot, scale, row and store for one token per request.
+template <bool FP8, int D, int BS, int WPU>
+__global__ void __launch_bounds__(kAppendThreads, 3) kda_cache_append_kernel(const CacheAppendParams p)
 {
-    constexpr int WPU = BS / 16, UNITS = 8 / WPU;         // warps of a unit, units of a CTA
+    constexpr int UNITS = 8 / WPU, CHUNKS = BS / 16 / WPU;        // units of a CTA; 16-token pieces of a warp
     constexpr int LPT = D / 4, TPS = 32 / LPT, STEPS = 16 / TPS;  // lanes of a token, tokens of a step
     __shared__ uint32_t tops[8];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane / LPT;
     const int groups = (2 * p.HKV + UNITS - 1) / UNITS;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / groups) * p.window;
     const int unit = (blockIdx.x % groups) * UNITS + warp / WPU, ws = warp % WPU;
     const bool live = unit < 2 * p.HKV;
     const int kv = unit & 1, h = min(unit >> 1, p.HKV - 1);
-    const __nv_bfloat16 *in = kv ? p.x[1] : p.x[0];
     const int64_t stride = kv ? p.stride[1] : p.stride[0];
+    const __nv_bfloat16 *in = (kv ? p.x[1] : p.x[0]) + h * D + 4 * (lane % LPT);
     uint8_t *cache = kv ? p.cache[1] : p.cache[0];
     float *scale = kv ? p.scale[1] : p.scale[0];
     const int slots = p.num_blocks * BS;
-    for (int64_t t = t0; t < min(t0 + p.window, static_cast<int64_t>(p.T)); ++t) {
-        const int lead = p.slots[t];
-        if (lead < 0) continue;
-        if (lead >= slots) {
-            if (tid == 0) atomicOr(p.err, ERR_BLOCK_ID);
-            continue;
+    const int64_t t_end = min(t0 + p.window, static_cast<int64_t>(p.T));
+    // the leaders among 32 tokens at a time
+    uint32_t leads = 0;
+    int s_lane = -1;
+    int64_t base = t0 - 32;
+    for (;;) {
+        while (leads == 0) {
+            base += 32;
+            if (base >= t_end) return;
+            const int64_t at = base + lane;
+            s_lane = at < t_end ? p.slots[at] : -1;
+            int before = __shfl_up_sync(0xffffffffu, s_lane, 1);
+            if (lane == 0) before = base > 0 ? p.slots[base - 1] : -1;
+            if (s_lane >= slots) {
+                if (blockIdx.x % groups == 0 && warp == 0) atomicOr(p.err, ERR_BLOCK_ID);
+                s_lane = -1;
+            }
+            leads = __ballot_sync(0xffffffffu, s_lane >= 0 && (before < 0 || before / BS != s_lane / BS));
         }
-        const int blk = lead / BS;
-        if (t > 0) {
-            const int before = p.slots[t - 1];
-            if (before >= 0 && before / BS == blk) continue;
-        }
-        // this warp's 16 tokens of the run: offset in the block (or -1), and whether all before it belong to the run
-        int off = -1;
-        bool whole = true;
-#pragma unroll
-        for (int w = 0; w < WPU; ++w) {
-            const int64_t at = t + 16 * w + lane;
-            const int s = whole && w <= ws && lane < 16 && at < p.T ? p.slots[at] : -1;
-            const bool in = s >= 0 && s / BS == blk;
-            const uint32_t m = __ballot_sync(0xffffffffu, in) & 0xffffu;
-            const int n = whole && w <= ws ? __ffs(~m) - 1 : 0;  // leading tokens that belong to it
-            if (w == ws) off = lane < n ? s % BS : -1;
-            whole = whole && n == 16;
-        }
-        const __nv_bfloat16 *src = in + (t + 16 * ws) * stride + h * D + 4 * (lane % LPT);
-        uint2 x[STEPS];
-        int o[STEPS];
-        uint32_t top2 = 0;  // largest |x| of either half, as bf16 pairs
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int k = i * TPS + lane / LPT;
-            o[i] = __shfl_sync(0xffffffffu, off, k);
-            x[i] = make_uint2(0u, 0u);
-            if (live && o[i] >= 0) x[i] = *reinterpret_cast<const uint2 *>(src + k * stride);
-        }
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            // max drops NaN
-            asm("max.bf16x2 %0, %0, %1;\n" : "+r"(top2) : "r"(x[i].x & 0x7fff7fffu));
-            asm("max.bf16x2 %0, %0, %1;\n" : "+r"(top2) : "r"(x[i].y & 0x7fff7fffu));
-        }
-        uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // bits of non-negative bf16 order as integers
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top >= 0x7f80u) {  // infinities saturate: the maximum is over the finite values
-            top = 0;
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t a = ((e & 2 ? x[i].y : x[i].x) >> (16 * (e & 1))) & 0x7fffu;
-                    if (a < 0x7f80u) top = max(top, a);
-                }
-            top = __reduce_max_sync(0xffffffffu, top);
-        }
-        const int first = lead % BS;  // tokens of the block before the run: kept
+        const int bit = __ffs(leads) - 1;
+        leads &= leads - 1;
+        const int64_t t = base + bit;
+        const int lead = __shfl_sync(0xffffffffu, s_lane, bit);
+        const int blk = lead / BS, first = lead % BS;  // tokens of the block before the run are kept
         float *sp = scale + static_cast<int64_t>(blk) * p.HKV + h;
         const float was = first > 0 ? *sp : 0.f;
+        // 16 tokens of the run from its token 16 * piece on: this lane's offset in the block, or -1 behind the run
+        bool whole = true;
+        auto offsets = [&](int piece) {
+            const int64_t at = t + 16 * piece + lane;
+            const int s = whole && lane < 16 && at < p.T ? p.slots[at] : -1;
+            const uint32_t m = __ballot_sync(0xffffffffu, s >= 0 && s / BS == blk) & 0xffffu;
+            const int n = whole ? __ffs(~m) - 1 : 0;
+            whole = n == 16;
+            return lane < n ? s % BS : -1;
+        };
+        // a whole piece of consecutive slots needs no lookups
+        auto straight = [&](int off) {
+            const int o0 = __shfl_sync(0xffffffffu, off, 0);
+            return __all_sync(0xffffffffu, lane >= 16 || (off >= 0 && off == o0 + lane)) != 0;
+        };
+        uint2 x[STEPS];
+        auto load = [&](int piece, int off) {
+            const __nv_bfloat16 *src = in + (t + 16 * piece + sub) * stride;
+            if (straight(off)) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i, src += TPS * stride)
+                    x[i] = live ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i, src += TPS * stride) {
+                const int o = __shfl_sync(0xffffffffu, off, i * TPS + sub);
+                x[i] = make_uint2(0u, 0u);
+                if (live && o >= 0) x[i] = *reinterpret_cast<const uint2 *>(src);
+            }
+        };
+        // largest |x| as bits (those of non-negative bf16 order as integers)
+        int off = -1, pieces = 0;
+        uint32_t top2 = 0;
+        for (int w = 0; w < ws; ++w) offsets(w);
+#pragma unroll 1
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int o = offsets(c * WPU + ws);
+            if (c > 0 && !__any_sync(0xffffffffu, o >= 0)) break;
+            load(c * WPU + ws, o);
+            off = o;
+            pieces = c + 1;
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+                top2 = __vmaxu2(top2, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+            if (!whole) break;
+        }
+        uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+        const bool fine = top < 0x7f80u;
+        const bool again = CHUNKS > 1 && pieces > 1;  // only the last piece's rows are still in registers
+        if (!fine) {  // infinities and NaN do not count
+            top = 0;
+            whole = true;
+            for (int w = 0; w < ws; ++w) offsets(w);
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int o16 = offsets(c * WPU + ws);
+#pragma unroll 1
+                for (int k = sub; k < 16; k += TPS) {
+                    if (__shfl_sync(0xffffffffu, o16, k) < 0) continue;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(in + (t + 16 * (c * WPU + ws) + k) * stride);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a = ((e & 2 ? v.y : v.x) >> (16 * (e & 1))) & 0x7fffu;
+                        if (a < 0x7f80u) top = max(top, a);
+                    }
+                }
+                if (!whole) break;
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
         if (WPU > 1) {
             __syncthreads();  // (also: the run before has read tops)
             if (lane == 0) tops[warp] = top;
@@ -259,19 +335,56 @@ __global__ void __launch_bounds__(kAppendThreads) kda_cache_append_kernel(const 
         uint8_t *dst = cache + blk * p.block_stride + static_cast<int64_t>(h) * BS * D + 4 * (lane % LPT);
         if (first > 0 && s != was) {  // the earlier tokens' codes at the new scale
             const float r = was / s;
-            for (int k = ws * TPS + lane / LPT; k < first; k += WPU * TPS) {
+#pragma unroll 4
+            for (int k = ws * TPS + sub; k < first; k += WPU * TPS) {
                 uint32_t *c = reinterpret_cast<uint32_t *>(dst + k * D);
                 const float4 v = decode4<FP8>(*c);
                 *c = encode4<FP8>(v.x * r, v.y * r, v.z * r, v.w * r);
             }
         }
         const float inv = 1.f / s;
+        auto store = [&](int o16) {
+            if (straight(o16)) {
+                uint8_t *row = dst + (__shfl_sync(0xffffffffu, o16, 0) + sub) * D;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            if (o[i] >= 0)
-                *reinterpret_cast<uint32_t *>(dst + o[i] * D) =
-                    encode4<FP8>(bf16lo(x[i].x) * inv, bf16hi(x[i].x) * inv, bf16lo(x[i].y) * inv,
-                                 bf16hi(x[i].y) * inv);
+                for (int i = 0; i < STEPS; ++i)
+                    *reinterpret_cast<uint32_t *>(row + i * TPS * D) = encode4<FP8>(x[i], inv);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int o = __shfl_sync(0xffffffffu, o16, i * TPS + sub);
+                if (o >= 0) *reinterpret_cast<uint32_t *>(dst + o * D) = encode4<FP8>(x[i], inv);
+            }
+        };
+        if (!fine) {  // token by token
+            whole = true;
+            for (int w = 0; w < ws; ++w) offsets(w);
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int o16 = offsets(c * WPU + ws);
+#pragma unroll 1
+                for (int k = sub; k < 16; k += TPS) {
+                    const int o = __shfl_sync(0xffffffffu, o16, k);
+                    if (o < 0) continue;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(in + (t + 16 * (c * WPU + ws) + k) * stride);
+                    *reinterpret_cast<uint32_t *>(dst + o * D) =
+                        encode4<FP8>(bf16lo(v.x) * inv, bf16hi(v.x) * inv, bf16lo(v.y) * inv, bf16hi(v.y) * inv);
+                }
+                if (!whole) break;
+            }
+        } else if (!again) {
+            store(off);
+        } else {
+            whole = true;
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int o = offsets(c);
+                load(c, o);
+                store(o);
+                if (!whole) break;
+            }
+        }
         if (ws == 0 && lane == 0) *sp = s;
     }
 }
