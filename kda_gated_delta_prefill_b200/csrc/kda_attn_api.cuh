@@ -375,10 +375,10 @@ namespace {
 
 // Query heads of a unit, and the most CTAs that a decode step uses, whatever the device.
 int decode_heads(int H, int HKV) { return H / HKV <= 8 ? 8 : 16; }
-int64_t decode_ctas(int B, int H, int HKV, int table_width, int block_size)
+int64_t decode_ctas(int B, int H, int HKV, int D, int table_width, int block_size)
 {
     const int64_t hb = decode_heads(H, HKV), chunks = (H / HKV + hb - 1) / hb;
-    const int64_t tiles = (static_cast<int64_t>(table_width) * block_size + kda::kAdTile - 1) / kda::kAdTile;
+    const int64_t tiles = (static_cast<int64_t>(table_width) * block_size + kda::ad_tile(D) - 1) / kda::ad_tile(D);
     const int64_t row = HKV * chunks;  // each factor may be near 2^31
     return tiles >= kda::kAdMaxCtas || row >= kda::kAdMaxCtas ? kda::kAdMaxCtas
                                                               : std::min<int64_t>(kda::kAdMaxCtas, B * (tiles * row));
@@ -395,7 +395,7 @@ extern "C" size_t kda_attention_decode_workspace_size(int B, int H, int HKV, int
     if (B <= 0 || H <= 0 || HKV <= 0 || H % HKV || (D != 64 && D != 128) || table_width <= 0 ||
         block_shift(block_size) < 0)
         return 0;
-    const int64_t ctas = decode_ctas(B, H, HKV, table_width, block_size);
+    const int64_t ctas = decode_ctas(B, H, HKV, D, table_width, block_size);
     return decode_part_bytes(ctas, H, HKV, D) + round_up(static_cast<size_t>(ctas) * sizeof(int2), kAlign);
 }
 
@@ -434,7 +434,7 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
     if (device_info(info) != cudaSuccess) return KDA_ERR_CUDA;
     using namespace kda;
     const int hb = decode_heads(H, HKV);
-    const int64_t ctas = decode_ctas(B, H, HKV, table_width, block_size);
+    const int64_t ctas = decode_ctas(B, H, HKV, D, table_width, block_size);
     AttnDecodeParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.q_stride = q_row_stride;
@@ -455,12 +455,12 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
     p.width = table_width;
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * kLog2e;
-    const int rows = std::min(block_size, kAdTile), shift = block_shift(block_size);
+    const int rows = std::min(block_size, ad_tile(D)), shift = block_shift(block_size);
     CUtensorMap mk, mv;
     if (!cache_map(&mk, k_cache, D, HKV * block_size, num_blocks, block_stride, rows) ||
         !cache_map(&mv, v_cache, D, HKV * block_size, num_blocks, block_stride, rows))
         return KDA_ERR_CUDA;
-    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(info.sms) * kAdCtasPerSm));
+    const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(info.sms) * ad_ctas(hb / 8)));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto go = [&](auto fp8, auto d, auto nt) {
         constexpr bool F = decltype(fp8)::value;

@@ -26,7 +26,12 @@
 
 namespace kda {
 
-constexpr int kAdTile = 64, kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512, kAdCtasPerSm = 2;
+// A tile is 16 KB of codes: 64 tokens at D = 128, 128 at D = 64, where a warp takes two slices of 16 tokens at once.
+// The warps' work on a tile is a chain of latencies (shared memory, MMAs, shuffles, exponentials, MMAs), so three CTAs
+// share an SM where registers allow it (up to 8 query heads): TODO measured.
+__host__ __device__ constexpr int ad_tile(int D) { return 64 * (128 / D); }
+__host__ __device__ constexpr int ad_ctas(int NT) { return NT == 1 ? 3 : 2; }
+constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
 
 struct AttnDecodeParams {
     const __nv_bfloat16 *q;  // row b at q + b * q_stride: [H, D]
@@ -47,26 +52,22 @@ struct AttnDecodeParams {
 template <int D, int NT>
 struct AttnDecodeSmem {
     static constexpr int HB = 8 * NT;                  // query heads of a unit
-    static constexpr int HALF = kAdTile * D;           // K or V codes of a tile
-    static constexpr int NST = (NT == 1 ? 5 : 4) * (128 / D);
+    static constexpr int SL = 128 / D;                 // slices of a warp
+    static constexpr int HALF = ad_tile(D) * D;        // K or V codes of a tile: 8 KB
+    static constexpr int NST = NT == 1 ? 3 : 4;
     static constexpr int JOIN = NST * 2 * HALF;        // fp32 [4 warps][HB][D]
-    static constexpr int STATS = JOIN + kAdWarps * HB * D * 4;   // fp32 [4 warps][HB][2]
-    static constexpr int META = STATS + kAdWarps * HB * 2 * 4;   // float4 [NST][4 slices]
-    static constexpr int SCAN = META + NST * kAdWarps * 16;      // int64 [5 warps], start {b, tile}
-    static constexpr int BAR = SCAN + 64 + 16;
-    static constexpr int ABORT = BAR + 2 * NST * 8;
+    static constexpr int QROWS = JOIN + kAdWarps * HB * D * 4;       // bf16 [2][HB][D]: queries of this unit and the next
+    static constexpr int STATS = QROWS + 2 * HB * D * 2;             // fp32 [4 warps][HB][2]
+    static constexpr int META = STATS + kAdWarps * HB * 2 * 4;       // float4 [NST][4 SL slices]
+    static constexpr int SCAN = META + NST * kAdWarps * SL * 16;     // int64 [5 warps], start {b, tile}
+    static constexpr int BAR = SCAN + 64 + 16;                       // full[NST] empty[NST] qfull[2] qempty[2]
+    static constexpr int ABORT = BAR + (2 * NST + 4) * 8;
     static constexpr int TOTAL = ABORT + 8;
 };
 
 // Where CTA c's share of W tiles begins.
 __device__ __forceinline__ int64_t share(int64_t W, int c, int G) { return W * c / G; }
 
-__device__ __forceinline__ void mma_f16_2(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1)
-{
-    const uint32_t a[4] = {a0, a1, a2, a3};
-    mma_f16(d, a, b0, b1);
-}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 {
     uint32_t y;
@@ -103,12 +104,13 @@ __device__ __forceinline__ void store_attention(const AttnDecodeParams &p, int b
 }
 
 template <bool FP8, int D, int NT>
-__global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
+__global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
     kda_attn_decode_kernel(const AttnDecodeParams p, const __grid_constant__ CUtensorMap mk,
                            const __grid_constant__ CUtensorMap mv, const int shift)
 {
     using S = AttnDecodeSmem<D, NT>;
-    constexpr int NST = S::NST, HB = S::HB, HALF = S::HALF, KS = D / 16, MT = D / 16;
+    constexpr int NST = S::NST, HB = S::HB, HALF = S::HALF, SL = S::SL, KS = D / 16, MT = D / 16;
+    constexpr int TILE = ad_tile(D), SLICES = TILE / 16, BATCH = 32 / SLICES;  // tiles whose pages the loader looks up at once
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -116,16 +118,20 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
     const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
     const int bs = 1 << shift;
     const int cap = static_cast<int>(min(static_cast<int64_t>(p.width) << shift, static_cast<int64_t>(INT_MAX) - 64));
-    const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST;
+    const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull0 = empty0 + 8 * NST, qempty0 = qfull0 + 16;
     float4 *meta = reinterpret_cast<float4 *>(sm + S::META);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     auto len_of = [&](int b) { return min(max(p.lens[b], 0), cap); };
-    auto tiles_of = [&](int b) { return (len_of(b) + kAdTile - 1) / kAdTile; };
+    auto tiles_of = [&](int b) { return (len_of(b) + TILE - 1) / TILE; };
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, kAdWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(qfull0 + 8 * s, 1);
+            mbar_init(qempty0 + 8 * s, kAdWarps);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -188,22 +194,34 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
     };
 
     if (warp == kAdWarps) {
-        // ---------------- loads: lane = tile (of 8) * 4 + slice of 16 tokens ----------------
-        const int slices_page = bs / 16, rows = min(bs, kAdTile);   // slices of a page; rows of one copy
-        int it = 0;
+        // ---------------- loads: lane = tile of a batch * SLICES + slice of 16 tokens ----------------
+        const int slices_page = min(bs / 16, SLICES), rows = 16 * slices_page;  // slices and rows of one copy
+        const int my_tile = lane / SLICES, my_slice = lane % SLICES;
+        int it = 0, pieces = 0;
         bool ok = true;
         while (left > 0 && ok) {
             const int t1 = static_cast<int>(min(static_cast<int64_t>(n), t0 + left));
-            const int len = len_of(b), hk = u / p.chunks;
-            auto ids = [&](int t) {  // the block of this lane's slice, tiles t .. t + 7
-                const int tok = (t + (lane >> 2)) * kAdTile + 16 * (lane & 3);
-                if (t + (lane >> 2) >= t1 || tok >= len) return -2;
+            const int len = len_of(b), hk = u / p.chunks, hc = u % p.chunks;
+            auto ids = [&](int t) {  // the block of this lane's slice
+                const int tok = (t + my_tile) * TILE + 16 * my_slice;
+                if (t + my_tile >= t1 || tok >= len) return -2;
                 const int id = p.table[b * p.table_stride + (tok >> shift)];
                 return id >= 0 && id < p.num_blocks ? id : -1;
             };
             int id = ids(t0);
-            for (int t = t0; t < t1 && ok; t += 8) {
-                const int far = ids(t + 8);
+            // the unit's queries: its heads stand beside one another in the row
+            const int qs = pieces & 1;
+            if (pieces >= 2) ok = __all_sync(0xffffffffu, mbar_wait(qempty0 + 8 * qs, ((pieces >> 1) - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                const int bytes = min(HB, group - hc * HB) * D * 2;
+                mbar_expect_tx(qfull0 + 8 * qs, bytes);
+                bulk_load(sb + S::QROWS + qs * HB * D * 2, p.q + b * p.q_stride + (hk * group + hc * HB) * D, bytes,
+                          qfull0 + 8 * qs);
+            }
+            ++pieces;
+            for (int t = t0; t < t1 && ok; t += BATCH) {
+                const int far = ids(t + BATCH);
                 float ks = 0.f, vs = 0.f;
                 if (id >= 0) {
                     ks = p.kscale[static_cast<int64_t>(id) * p.HKV + hk];
@@ -214,10 +232,9 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
                 // values are zero where its scale is: any scale will do then
                 const float v1 = vs > 0.f ? vs : 1.f;
                 const float4 m = make_float4(ks, log2f(v1), 1.f / v1, id >= 0 ? (vs > 0.f ? 1.f : 2.f) : 0.f);
-                // the lane that copies: the first slice of a page, or of a tile inside a longer page
-                const bool copies = id >= 0 && (slices_page >= 4 ? (lane & 3) == 0 : (lane & 3) % slices_page == 0);
+                const bool copies = id >= 0 && my_slice % slices_page == 0;  // the lane of a copy's first slice
                 const uint32_t who = __ballot_sync(0xffffffffu, copies);
-                for (int k = 0; k < 8 && t + k < t1; ++k, ++it) {
+                for (int k = 0; k < BATCH && t + k < t1; ++k, ++it) {
                     const int st = it % NST;
                     if (it >= NST) {
                         ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * st, ((it / NST) - 1) & 1));
@@ -226,14 +243,14 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
                             break;
                         }
                     }
-                    if ((lane >> 2) == k) meta[st * kAdWarps + (lane & 3)] = m;
+                    if (my_tile == k) meta[st * SLICES + my_slice] = m;
                     __syncwarp();
-                    const uint32_t mine4 = (who >> (4 * k)) & 15u;
-                    if (lane == 0) mbar_expect_tx(full0 + 8 * st, __popc(mine4) * 2 * rows * D);
+                    const int copies_k = __popc((who >> (SLICES * k)) & ((1u << SLICES) - 1));
+                    if (lane == 0) mbar_expect_tx(full0 + 8 * st, copies_k * 2 * rows * D);
                     __syncwarp();
-                    if ((lane >> 2) == k && copies) {
-                        const int tok = (t + k) * kAdTile + 16 * (lane & 3);
-                        const uint32_t dst = sb + st * 2 * HALF + 16 * (lane & 3) * D;
+                    if (my_tile == k && copies) {
+                        const int tok = (t + k) * TILE + 16 * my_slice;
+                        const uint32_t dst = sb + st * 2 * HALF + 16 * my_slice * D;
                         const int row = hk * bs + (tok & (bs - 1));
                         tma_load_3d(dst, &mk, 0, row, id, full0 + 8 * st);
                         tma_load_3d(dst + HALF, &mv, 0, row, id, full0 + 8 * st);
@@ -249,26 +266,30 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
                 *abort_flag = 1;
             }
             for (int i = max(0, it - NST); i < it; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
+            for (int i = max(0, pieces - 2); i < pieces; ++i) mbar_wait(qfull0 + 8 * (i & 1), (i >> 1) & 1);
         }
         return;
     }
 
-    // ---------------- arithmetic: warp w takes slice w of every tile ----------------
+    // ---------------- arithmetic: warp w takes slices SL w .. SL w + SL - 1 of every tile ----------------
     const int r = lane >> 2, cc = lane & 3;
     float *join = reinterpret_cast<float *>(sm + S::JOIN), *stats = reinterpret_cast<float *>(sm + S::STATS);
-    int it = 0;
+    int it = 0, pieces = 0;
     bool ok = true;
     while (left > 0) {
         const int t1 = static_cast<int>(min(static_cast<int64_t>(n), t0 + left));
         const int len = len_of(b), hk = u / p.chunks, hc = u % p.chunks;
         const int heads = min(HB, group - hc * HB), head0 = hk * group + hc * HB;
+        const int qs = pieces & 1;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(qfull0 + 8 * qs, (pieces >> 1) & 1));
+        ++pieces;
         // query rows as B operands: column r (head), the dims that this lane's K words hold
         uint32_t qf[NT][KS][2];
         float f0[NT], f1[NT];  // score factors of heads 2 cc and 2 cc + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int hd = 8 * nt + r;
-            const __nv_bfloat16 *src = p.q + b * p.q_stride + static_cast<int64_t>(head0 + hd) * D + cc * (D / 4);
+            const uint8_t *src = sm + S::QROWS + ((qs * HB + hd) * D + cc * (D / 4)) * 2;
             uint4 raw[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -294,6 +315,7 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
             f0[nt] = __shfl_sync(0xffffffffu, f, 8 * cc);
             f1[nt] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
         }
+        if (ok && lane == 0) mbar_arrive(qempty0 + 8 * qs);
         float acc[NT][MT][4], M0[NT], M1[NT], l0[NT], l1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -307,67 +329,70 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
             const int st = it % NST;
             ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * st, (it / NST) & 1));
             if (!ok) break;
-            const float4 m = meta[st * kAdWarps + warp];
-            const int have = len - t * kAdTile - 16 * warp;  // tokens of the slice
-            if (have > 0 && m.w != 0.f) {
-                const uint8_t *kt = sm + st * 2 * HALF, *vt = kt + HALF;
-                const int row = 16 * warp + r;
-                uint32_t kw[2][D / 16];  // token r and r + 8: the words of this lane's D / 4 dims
+            const uint8_t *kt = sm + st * 2 * HALF, *vt = kt + HALF;
+            float4 m[SL];
+            int have[SL];  // tokens of the slice
+            bool counts = false;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rw = row + 8 * i;
+            for (int y = 0; y < SL; ++y) {
+                m[y] = meta[st * SLICES + SL * warp + y];
+                have[y] = m[y].w != 0.f ? len - t * TILE - 16 * (SL * warp + y) : 0;
+                counts = counts || have[y] > 0;
+            }
+            if (counts) {
+                float s[SL][NT][4];
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j) {
-                        const int ch = D == 128 ? ((2 * cc + j) ^ (rw & 7)) : (cc ^ ((rw >> 1) & 3));
-                        const uint4 v = *reinterpret_cast<const uint4 *>(kt + rw * D + 16 * ch);
-                        kw[i][4 * j] = v.x;
-                        kw[i][4 * j + 1] = v.y;
-                        kw[i][4 * j + 2] = v.z;
-                        kw[i][4 * j + 3] = v.w;
+                for (int y = 0; y < SL; ++y) {
+                    uint32_t kw[2][KS];  // token r and r + 8: the words of this lane's D / 4 dims
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int rw = 16 * (SL * warp + y) + r + 8 * i;
+#pragma unroll
+                        for (int j = 0; j < D / 64; ++j) {
+                            const int ch = D == 128 ? ((2 * cc + j) ^ (rw & 7)) : (cc ^ ((rw >> 1) & 3));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(kt + rw * D + 16 * ch);
+                            kw[i][4 * j] = v.x;
+                            kw[i][4 * j + 1] = v.y;
+                            kw[i][4 * j + 2] = v.z;
+                            kw[i][4 * j + 3] = v.w;
+                        }
                     }
-                }
-                float s[NT][4];
+                    // two chains of MMAs, half as long
+                    float s1[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_f16<FP8>(kw[0][k], a0, a2);
-                    codes_to_f16<FP8>(kw[1][k], a1, a3);
+                        for (int e = 0; e < 4; ++e) s[y][nt][e] = s1[nt][e] = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16_2(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
-                }
-                // V words: tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9; dims of chunk r
-                uint32_t vw[4][D / 32];
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t a[4];
+                        codes_to_f16<FP8>(kw[0][k], a[0], a[2]);
+                        codes_to_f16<FP8>(kw[1][k], a[1], a[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 2 * cc + (i & 1) + 8 * (i >> 1), rw = 16 * warp + tok;
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vt + rw * D + 16 * (r ^ (rw & 7)));
-                        vw[i][0] = v.x;
-                        vw[i][1] = v.y;
-                        vw[i][2] = v.z;
-                        vw[i][3] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(
-                            vt + rw * D + 16 * ((r >> 1) ^ ((rw >> 1) & 3)) + 8 * (r & 1));
-                        vw[i][0] = v.x;
-                        vw[i][1] = v.y;
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(k & 1 ? s1[nt] : s[y][nt], a, qf[nt][k][0], qf[nt][k][1]);
                     }
-                    // codes behind the last token, and of a block without a scale, may be anything
-                    if (tok >= have || m.w == 2.f)
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) vw[i][k] = 0u;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[y][nt][e] += s1[nt][e];
                 }
-                uint32_t pb[NT][2];
+                uint32_t pb[SL][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float a = f0[nt] * m.x, bq = f1[nt] * m.x;
-                    float x0 = fmaf(s[nt][0], a, m.y), x1 = fmaf(s[nt][1], bq, m.y);
-                    float x2 = fmaf(s[nt][2], a, m.y), x3 = fmaf(s[nt][3], bq, m.y);
-                    if (r >= have) x0 = x1 = -INFINITY;
-                    if (r + 8 >= have) x2 = x3 = -INFINITY;
-                    float h0 = fmaxf(x0, x2), h1 = fmaxf(x1, x3);
+                    float h0 = -INFINITY, h1 = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < SL; ++y) {
+                        const float a = f0[nt] * m[y].x, bq = f1[nt] * m[y].x;
+                        float(&x)[4] = s[y][nt];
+                        x[0] = fmaf(x[0], a, m[y].y);
+                        x[1] = fmaf(x[1], bq, m[y].y);
+                        x[2] = fmaf(x[2], a, m[y].y);
+                        x[3] = fmaf(x[3], bq, m[y].y);
+                        if (r >= have[y]) x[0] = x[1] = -INFINITY;
+                        if (r + 8 >= have[y]) x[2] = x[3] = -INFINITY;
+                        h0 = fmaxf(h0, fmaxf(x[0], x[2]));
+                        h1 = fmaxf(h1, fmaxf(x[1], x[3]));
+                    }
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
                         h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, off));
@@ -390,30 +415,61 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
                         }
                     }
                     const float e0 = 12.f - M0[nt], e1 = 12.f - M1[nt];
-                    x0 = ex2(x0 + e0);
-                    x1 = ex2(x1 + e1);
-                    x2 = ex2(x2 + e0);
-                    x3 = ex2(x3 + e1);
-                    l0[nt] = fmaf(x0 + x2, m.z, l0[nt]);
-                    l1[nt] = fmaf(x1 + x3, m.z, l1[nt]);
-                    pb[nt][0] = movmatrix(pack_f16(x0, x1));
-                    pb[nt][1] = movmatrix(pack_f16(x2, x3));
+#pragma unroll
+                    for (int y = 0; y < SL; ++y) {
+                        float(&x)[4] = s[y][nt];
+                        x[0] = ex2(x[0] + e0);
+                        x[1] = ex2(x[1] + e1);
+                        x[2] = ex2(x[2] + e0);
+                        x[3] = ex2(x[3] + e1);
+                        if (SL > 1 && have[y] <= 0) x[0] = x[1] = x[2] = x[3] = 0.f;  // (before any token: M is -inf)
+                        l0[nt] = fmaf(x[0] + x[2], m[y].z, l0[nt]);
+                        l1[nt] = fmaf(x[1] + x[3], m[y].z, l1[nt]);
+                        pb[y][nt][0] = movmatrix(pack_f16(x[0], x[1]));
+                        pb[y][nt][1] = movmatrix(pack_f16(x[2], x[3]));
+                    }
                 }
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    // bytes of two tokens side by side: A operand pairs along the tokens
-                    uint32_t a[2][4];  // dims 4 w + {0, 1} and {2, 3} of the chunk: a0 a1 a2 a3
+                for (int y = 0; y < SL; ++y) {
+                    // V words: tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9; dims of chunk r
+                    uint32_t vw[4][D / 32];
 #pragma unroll
-                    for (int pr = 0; pr < 2; ++pr) {
-                        const uint32_t lo = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x5140);
-                        const uint32_t hi = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x7362);
-                        codes_to_f16<FP8>(lo, a[0][2 * pr], a[0][2 * pr + 1]);
-                        codes_to_f16<FP8>(hi, a[1][2 * pr], a[1][2 * pr + 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 2 * cc + (i & 1) + 8 * (i >> 1), rw = 16 * (SL * warp + y) + tok;
+                        if constexpr (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(vt + rw * D + 16 * (r ^ (rw & 7)));
+                            vw[i][0] = v.x;
+                            vw[i][1] = v.y;
+                            vw[i][2] = v.z;
+                            vw[i][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(
+                                vt + rw * D + 16 * ((r >> 1) ^ ((rw >> 1) & 3)) + 8 * (r & 1));
+                            vw[i][0] = v.x;
+                            vw[i][1] = v.y;
+                        }
+                        // codes behind the last token, and of a block without a scale, may be anything
+                        if (tok >= have[y] || m[y].w == 2.f)
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k) vw[i][k] = 0u;
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int w = 0; w < D / 32; ++w) {
+                        // bytes of two tokens side by side: A operand pairs along the tokens
+                        uint32_t a[2][4];  // dims 4 w + {0, 1} and {2, 3} of the chunk: a0 a1 a2 a3
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + i], a[i], pb[nt][0], pb[nt][1]);
+                        for (int pr = 0; pr < 2; ++pr) {
+                            const uint32_t lo = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x5140);
+                            const uint32_t hi = __byte_perm(vw[2 * pr][w], vw[2 * pr + 1][w], 0x7362);
+                            codes_to_f16<FP8>(lo, a[0][2 * pr], a[0][2 * pr + 1]);
+                            codes_to_f16<FP8>(hi, a[1][2 * pr], a[1][2 * pr + 1]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(acc[nt][2 * w + i], a[i], pb[y][nt][0], pb[y][nt][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -423,7 +479,8 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
             atomicOr(p.err, ERR_PIPE_FULL_WAIT);
             *abort_flag = 1;
         }
-        // ---------------- join the four warps ----------------
+        // ---------------- join the four warps (the unit before has been read) ----------------
+        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -479,7 +536,6 @@ __global__ void __launch_bounds__(kAdThreads, kAdCtasPerSm)
             while (share(W, k, G) > end) --k;
             p.shared_unit[c] = make_int2(b * units_row + u, k - c);
         }
-        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
         next(t1);
     }
 }
