@@ -159,6 +159,25 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, 
     }
 }
 
+// 2^x for pairs on the FMA and integer pipes, beside the special-function unit, whose 16 results a cycle are what a
+// softmax runs out of first: x = n + f with n the nearest integer, 2^f by a polynomial, n added to the exponent.
+// The polynomial is the minimax one of degree 4 on [-1/2, 1/2] (Remez): relative error below 2.6e-6.  x is clamped at
+// -125.5, below which the result would leave the normal range.
+__device__ __forceinline__ float2 exp2_poly(float2 x)
+{
+    const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
+    x = make_float2(fmaxf(x.x, -125.5f), fmaxf(x.y, -125.5f));
+    const float2 t = add2(x, magic);  // the low bits hold n
+    const float2 n = add2(t, unmagic);
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+    float2 q = fma2(f, make_float2(0.009570102f, 0.009570102f), make_float2(0.05591786f, 0.05591786f));
+    q = fma2(q, f, make_float2(0.24024744f, 0.24024744f));
+    q = fma2(q, f, make_float2(0.6931218f, 0.6931218f));
+    q = fma2(q, f, make_float2(0.9999993f, 0.9999993f));
+    return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 }  // namespace kda

@@ -17,6 +17,8 @@
 // tensor cores work on the other tile.  S of the next key tile is issued behind O += P V of this one (they share
 // columns), so a softmax warp that sees S may also rescale O: no MMA writes it then.
 #pragma once
+#include <type_traits>
+
 #include "kda_attn_common.cuh"
 
 namespace kda {
@@ -35,8 +37,8 @@ struct AttnFwdSmem {
     static constexpr int TILE = AT * D * 2;
     static constexpr int NST = D == 128 ? 5 : 8;
     static constexpr int RING = 2 * TILE;
-    static constexpr int BAR = RING + NST * TILE;  // full[NST] empty[NST] qfull[2] sfull[2] pready[2] odone[2]
-    static constexpr int TMEM_SLOT = BAR + (2 * NST + 8) * 8;
+    static constexpr int BAR = RING + NST * TILE;  // full[NST] empty[NST] qfull[2] sfull[2] pready[2][2] odone[2]
+    static constexpr int TMEM_SLOT = BAR + (2 * NST + 10) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -44,6 +46,10 @@ struct AttnFwdSmem {
 // third warpgroup (two of its warps idle) keeps 88: 256 * 208 + 128 * 88 = 64,512.
 constexpr int kAttnFwdThreads = 384;
 constexpr int kAttnFwdRows = 2 * AT;
+#ifndef FWDPOLY
+#define FWDPOLY 4
+#endif
+constexpr int kAttnFwdPoly = FWDPOLY;
 
 template <int D>
 __global__ void __launch_bounds__(kAttnFwdThreads, 1)
@@ -74,7 +80,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     const int nmax = max(nt[0], nt[1]);
 
     const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull0 = empty0 + 8 * NST, sfull0 = qfull0 + 16,
-                   pready0 = qfull0 + 32, odone0 = qfull0 + 48;
+                   pready0 = qfull0 + 32, odone0 = qfull0 + 64;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -84,7 +90,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         for (int w = 0; w < 2; ++w) {
             mbar_init(qfull0 + 8 * w, 1);
             mbar_init(sfull0 + 8 * w, 1);
-            mbar_init(pready0 + 8 * w, 4);
+            mbar_init(pready0 + 16 * w, 4);
+            mbar_init(pready0 + 16 * w + 8, 4);
             mbar_init(odone0 + 8 * w, 1);
         }
         *abort_flag = 0;
@@ -120,7 +127,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             for (int i = 0; i < 4; ++i) tc_ld32(ts + 32 * i, r[i]);
             tc_wait_ld();
             const int keys = seen - j * AT;
-            if (__any_sync(0xffffffffu, keys < AT)) {
+            const bool cut = __any_sync(0xffffffffu, keys < AT);
+            if (cut) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -158,27 +166,38 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     }
                 }
             }
+            // P in two halves of 64 keys: the MMAs start on the first while the second is formed
             const float2 c2 = make_float2(c, c), b2 = make_float2(-m * c, -m * c);
             float2 sum = make_float2(0.f, 0.f), sum1 = sum;
+            auto half = [&](int hf, auto poly) {  // poly: pairs of 16 that take the polynomial
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pk[16];
+                for (int i = 2 * hf; i < 2 * hf + 2; ++i) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 x = fma2(make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])), c2, b2);
-                    x.x = ex2_ftz(x.x);
-                    x.y = ex2_ftz(x.y);
-                    if (e & 1) sum1 = add2(sum1, x);
-                    else sum = add2(sum, x);
-                    pk[e] = pack_bf16(x.x, x.y);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x =
+                            fma2(make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])), c2, b2);
+                        if (e % 4 < decltype(poly)::value / 4) x = exp2_poly(x);
+                        else x = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+                        if (e & 1) sum1 = add2(sum1, x);
+                        else sum = add2(sum, x);
+                        pk[e] = pack_bf16(x.x, x.y);
+                    }
+                    tc_st16(ts + 16 * i, pk);
                 }
-                tc_st16(ts + 16 * i, pk);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready0 + 8 * (2 * w + hf));
+            };
+            if (cut) {  // a masked score's weight is 0 exactly, which the clamped polynomial's is not
+                half(0, std::integral_constant<int, 0>{});
+                half(1, std::integral_constant<int, 0>{});
+            } else {
+                half(0, std::integral_constant<int, kAttnFwdPoly>{});
+                half(1, std::integral_constant<int, kAttnFwdPoly>{});
             }
             l += (sum.x + sum.y) + (sum1.x + sum1.y);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pready0 + 8 * w);
         }
         // ---------------- o = O / l, through this warp's rows of the Q tile (no MMA reads it any more) ----------------
         if (ok && nt[w] > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(odone0 + 8 * w, 0));
@@ -264,12 +283,17 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     zero_tail_rows<D>(sb + S::RING + (rv % NST) * TILE, sq.lk - j * AT, lane);
                 for (int w = 0; w < 2 && ok; ++w) {
                     if (j >= nt[w]) continue;
-                    if (!wait(pready0 + 8 * w, j & 1)) break;
                     const uint64_t b = vd + (rv % NST) * (TILE >> 4);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (!wait(pready0 + 8 * (2 * w + hf), j & 1)) break;
 #pragma unroll
-                    for (int ks = 0; ks < AT / 16; ++ks)
-                        tc_mma_ts_warp(tmem + TM_O + D * w, tmem + 128 * w + 8 * ks, b + kstep_mn(ks), id_o,
-                                       j > 0 || ks > 0);
+                        for (int k = 0; k < AT / 32; ++k) {
+                            const int ks = 4 * hf + k;
+                            tc_mma_ts_warp(tmem + TM_O + D * w, tmem + 128 * w + 8 * ks, b + kstep_mn(ks), id_o,
+                                           j > 0 || ks > 0);
+                        }
+                    }
+                    if (!ok) break;
                     if (j + 1 < nt[w]) {
                         if (!wait(full0 + 8 * (rk % NST), (rk / NST) & 1)) break;
                         score(w, rk);
