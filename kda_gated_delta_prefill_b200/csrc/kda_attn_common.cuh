@@ -10,6 +10,27 @@ namespace kda {
 // further bits of the device error word
 enum : unsigned { ERR_BLOCK_ID = 16u, ERR_CACHE_FULL = 32u };
 
+// Wait for a phase without taking issue slots from the scheduler's other warps: mbarrier.try_wait suspends the warp for a
+// time that the hardware chooses (with a long limit of one's own it also resumes late).  Bounded like mbar_wait.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity)
+{
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity))
+        if (clock64() - t0 > kWaitBudget) return false;
+    return true;
+}
+
 constexpr int AT = 128;  // rows of an attention tile, of queries and of keys
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -157,25 +178,6 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, 
                      : "r"(stage + rr * (D * 2) + ((ch ^ (rr & 7)) << 4)));
         *reinterpret_cast<uint4 *>(dst + rr * stride + 8 * ch) = u;
     }
-}
-
-// 2^x for pairs on the FMA and integer pipes, beside the special-function unit, whose 16 results a cycle are what a
-// softmax runs out of first: x = n + f with n the nearest integer, 2^f by a polynomial, n added to the exponent.
-// The polynomial is the minimax one of degree 4 on [-1/2, 1/2] (Remez): relative error below 2.6e-6.  x is clamped at
-// -125.5, below which the result would leave the normal range.
-__device__ __forceinline__ float2 exp2_poly(float2 x)
-{
-    const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
-    x = make_float2(fmaxf(x.x, -125.5f), fmaxf(x.y, -125.5f));
-    const float2 t = add2(x, magic);  // the low bits hold n
-    const float2 n = add2(t, unmagic);
-    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
-    float2 q = fma2(f, make_float2(0.009570102f, 0.009570102f), make_float2(0.05591786f, 0.05591786f));
-    q = fma2(q, f, make_float2(0.24024744f, 0.24024744f));
-    q = fma2(q, f, make_float2(0.6931218f, 0.6931218f));
-    q = fma2(q, f, make_float2(0.9999993f, 0.9999993f));
-    return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }

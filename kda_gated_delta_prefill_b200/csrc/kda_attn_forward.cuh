@@ -11,11 +11,21 @@
 //
 // One CTA takes 256 queries of one head as two tiles of 128 (A and B) and walks the key tiles of 128.
 //   warps 0-3, 4-7  softmax of tile A, B: a thread per row
-//   warp 8          issues the MMAs: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM)
-//   warp 9          TMA loads of Q, and of K and V tiles through a ring
-// TMEM: S_A, S_B (128 columns each, P in bf16 over their first half), O_A, O_B.  While one tile's softmax runs, the
-// tensor cores work on the other tile.  S of the next key tile is issued behind O += P V of this one (they share
-// columns), so a softmax warp that sees S may also rescale O: no MMA writes it then.
+//   warp 8 (and 9)  issues the MMAs: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM)
+//   warp 10         TMA loads of Q, and of K and V tiles through a ring
+// TMEM: S_A, S_B (128 columns each), O_A, O_B and, where there is room (D = 64), P_A and P_B.  P is handed over in halves
+// of 64 keys, so that O += P V starts while the second half is formed (at D = 128: 4.07 -> 3.46 ms for 32,768 tokens and 16
+// heads).
+//  D = 128: P lies over S, so S of the next key tile is issued behind O += P V of this one, and one warp issues for both
+//    tiles in turn, which keeps them half a period apart: while one is in its softmax, the tensor cores work on the other.
+//    A softmax warp that sees S may also rescale O: no MMA writes it then.
+//  D = 64: S of the next key tile is issued as soon as the softmax has read this one into registers, and each tile has its
+//    own issuer (0.69-0.75 ms for 16,384 tokens and 16 heads; 0.83 with P over S).
+// Bound at D = 64 by the exponentials (16 a cycle and SM: 2,048 cycles for both tiles, of about 2,700), and at D = 128, for
+// long sequences, by power: at 1,340 TFLOP/s the clock falls to 1.6 GHz.  Measured there without gain: a polynomial on the
+// FMA pipe for a quarter of the exponentials; scores in halves with N = 64, so that neither waits for the other (fewer
+// cycles, but Q read twice: less clock, 3.86 ms).  Waiting warps are suspended (mbarrier.try_wait): polling took issue slots
+// from the softmax (3.46 -> 3.36 ms).
 #pragma once
 #include <type_traits>
 
@@ -37,8 +47,8 @@ struct AttnFwdSmem {
     static constexpr int TILE = AT * D * 2;
     static constexpr int NST = D == 128 ? 5 : 8;
     static constexpr int RING = 2 * TILE;
-    static constexpr int BAR = RING + NST * TILE;  // full[NST] empty[NST] qfull[2] sfull[2] pready[2][2] odone[2]
-    static constexpr int TMEM_SLOT = BAR + (2 * NST + 10) * 8;
+    static constexpr int BAR = RING + NST * TILE;  // full[NST] empty[NST] qfull[2] sfull[2] pready[2][2] sfree[2] odone[2]
+    static constexpr int TMEM_SLOT = BAR + (2 * NST + 12) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -46,10 +56,6 @@ struct AttnFwdSmem {
 // third warpgroup (two of its warps idle) keeps 88: 256 * 208 + 128 * 88 = 64,512.
 constexpr int kAttnFwdThreads = 384;
 constexpr int kAttnFwdRows = 2 * AT;
-#ifndef FWDPOLY
-#define FWDPOLY 4
-#endif
-constexpr int kAttnFwdPoly = FWDPOLY;
 
 template <int D>
 __global__ void __launch_bounds__(kAttnFwdThreads, 1)
@@ -58,7 +64,9 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
 {
     using S = AttnFwdSmem<D>;
     constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
-    constexpr uint32_t TM_O = 256, TM_COLS = 512;
+    constexpr bool kOwnP = D == 64;          // P has columns of its own
+    constexpr int kIssuers = kOwnP ? 2 : 1;  // warps that issue MMAs
+    constexpr uint32_t TM_O = 256, TM_P = kOwnP ? 384 : 0, TM_PSTEP = kOwnP ? 64 : 128, TM_COLS = 512;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -80,18 +88,19 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     const int nmax = max(nt[0], nt[1]);
 
     const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull0 = empty0 + 8 * NST, sfull0 = qfull0 + 16,
-                   pready0 = qfull0 + 32, odone0 = qfull0 + 64;
+                   pready0 = qfull0 + 32, sfree0 = qfull0 + 64, odone0 = qfull0 + 80;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, kIssuers);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(qfull0 + 8 * w, 1);
             mbar_init(sfull0 + 8 * w, 1);
             mbar_init(pready0 + 16 * w, 4);
             mbar_init(pready0 + 16 * w + 8, 4);
+            mbar_init(sfree0 + 8 * w, 4);
             mbar_init(odone0 + 8 * w, 1);
         }
         *abort_flag = 0;
@@ -112,20 +121,25 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         const int w = warp >> 2, quarter = warp & 3;
         const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t ts = tmem + lb + 128 * w, to = tmem + lb + TM_O + D * w;
+        const uint32_t ts = tmem + lb + 128 * w, tp = tmem + lb + TM_P + TM_PSTEP * w, to = tmem + lb + TM_O + D * w;
         const int row = r0 + w * AT + 32 * quarter + lane;
         const int seen = min(row, sq.lq - 1) + 1 + diff;  // keys that the row sees (rows past the end: any)
         const float c = p.scale_log2;
         float m = 0.f, l = 0.f;  // reference (in units of the scores), sum
         bool ok = true;
         for (int j = 0; j < nt[w]; ++j) {
-            ok = __all_sync(0xffffffffu, mbar_wait_spin(sfull0 + 8 * w, j & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(sfull0 + 8 * w, j & 1));
             if (!ok) break;
             tc_fence_after();
             uint32_t r[4][32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) tc_ld32(ts + 32 * i, r[i]);
             tc_wait_ld();
+            if (kOwnP) {  // the next scores may be formed
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfree0 + 8 * w);
+            }
             const int keys = seen - j * AT;
             const bool cut = __any_sync(0xffffffffu, keys < AT);
             if (cut) {
@@ -150,6 +164,11 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             } else {
                 // a row that has seen no key yet (l == 0) takes its first finite maximum as the reference
                 const bool grow = (top - m) * c > 8.f || (l == 0.f && top != -INFINITY);
+                if (kOwnP) {  // O += P V of the tile before has read P and written O
+                    ok = __all_sync(0xffffffffu, mbar_wait_quiet(odone0 + 8 * w, (j - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mn = grow ? top : m;
                     const float alpha = l == 0.f ? 0.f : ex2((m - mn) * c);
@@ -169,38 +188,30 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             // P in two halves of 64 keys: the MMAs start on the first while the second is formed
             const float2 c2 = make_float2(c, c), b2 = make_float2(-m * c, -m * c);
             float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-            auto half = [&](int hf, auto poly) {  // poly: pairs of 16 that take the polynomial
 #pragma unroll
-                for (int i = 2 * hf; i < 2 * hf + 2; ++i) {
-                    uint32_t pk[16];
+            for (int i = 0; i < 4; ++i) {
+                uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 x =
-                            fma2(make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])), c2, b2);
-                        if (e % 4 < decltype(poly)::value / 4) x = exp2_poly(x);
-                        else x = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
-                        if (e & 1) sum1 = add2(sum1, x);
-                        else sum = add2(sum, x);
-                        pk[e] = pack_bf16(x.x, x.y);
-                    }
-                    tc_st16(ts + 16 * i, pk);
+                for (int e = 0; e < 16; ++e) {
+                    float2 x =
+                        fma2(make_float2(__uint_as_float(r[i][2 * e]), __uint_as_float(r[i][2 * e + 1])), c2, b2);
+                    x = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+                    if (e & 1) sum1 = add2(sum1, x);
+                    else sum = add2(sum, x);
+                    pk[e] = pack_bf16(x.x, x.y);
                 }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pready0 + 8 * (2 * w + hf));
-            };
-            if (cut) {  // a masked score's weight is 0 exactly, which the clamped polynomial's is not
-                half(0, std::integral_constant<int, 0>{});
-                half(1, std::integral_constant<int, 0>{});
-            } else {
-                half(0, std::integral_constant<int, kAttnFwdPoly>{});
-                half(1, std::integral_constant<int, kAttnFwdPoly>{});
+                tc_st16(tp + 16 * i, pk);
+                if (i & 1) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pready0 + 8 * (2 * w + (i >> 1)));
+                }
             }
             l += (sum.x + sum.y) + (sum1.x + sum1.y);
         }
         // ---------------- o = O / l, through this warp's rows of the Q tile (no MMA reads it any more) ----------------
-        if (ok && nt[w] > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(odone0 + 8 * w, 0));
+        if (ok && nt[w] > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(odone0 + 8 * w, kOwnP ? (nt[w] - 1) & 1 : 0));
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else {
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (warp == 9) {
+        if (warp == 10) {
             // ---------------- loads: Q_A, K_0, Q_B, V_0, K_1, V_1, ... ----------------
             if (lane == 0) {
                 const int hk = h / (p.H / p.HKV);
@@ -255,57 +266,72 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     }
                 }
             }
-        } else if (warp == 8) {
-            // ---------------- MMAs ----------------
-            const uint32_t id_s = idesc_bf16(128, AT, false, false), id_o = idesc_bf16(128, D, false, true);
-            const uint64_t qd = tile_desc_k(sb), kd = tile_desc_k(sb + S::RING), vd = tile_desc_mn(sb + S::RING);
-            bool ok = true;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
-                tc_fence_after();
-                return ok;
-            };
-            auto score = [&](int w, int ring) {  // S_w = Q_w K^T
-                const uint64_t a = qd + w * (TILE >> 4), b = kd + (ring % NST) * (TILE >> 4);
+        } else if (warp < 8 + kIssuers) {
+            // ---------------- MMAs of both tiles in turn, or of one each ----------------
+            auto issue = [&](auto first, auto last) {
+                constexpr int w0 = decltype(first)::value, w1 = decltype(last)::value;
+                constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_o = idesc_bf16(128, D, false, true);
+                // descriptors: a constant high word, and a low word that only offsets below 2^18 bytes are added to
+                const uint64_t dk = tile_desc_k(sb), dm = tile_desc_mn(sb);
+                const uint32_t khi = static_cast<uint32_t>(dk >> 32), klo = static_cast<uint32_t>(dk);
+                const uint32_t mhi = static_cast<uint32_t>(dm >> 32), mlo = static_cast<uint32_t>(dm);
+                auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+                bool ok = true;
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_quiet(bar, parity));
+                    tc_fence_after();
+                    return ok;
+                };
+                // ring positions: K_j at 2 j, V_j at 2 j + 1
+                auto arrived = [&](int pos) { return wait(full0 + 8 * (pos % NST), (pos / NST) & 1); };
+                auto release = [&](int pos) { tc_commit_warp(empty0 + 8 * (pos % NST)); };
+                auto score = [&](int w, int j) {  // S_w = Q_w K_j^T
+                    if (!arrived(2 * j)) return;
+                    const uint32_t b = klo + ((S::RING + ((2 * j) % NST) * TILE) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss_warp(tmem + 128 * w, a + kstep_k(ks), b + kstep_k(ks), id_s, ks > 0);
-                tc_commit_warp(sfull0 + 8 * w);
-            };
-            // ring positions: K_j at 2 j, V_j at 2 j + 1
-            for (int w = 0; w < 2 && ok; ++w)
-                if (nt[w] > 0 && wait(qfull0 + 8 * w, 0) && wait(full0, 0)) score(w, 0);
-            if (nmax > 0) tc_commit_warp(empty0);
-            for (int j = 0; j < nmax && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
-                const int rv = 2 * j + 1, rk = 2 * j + 2;
-                if (!wait(full0 + 8 * (rv % NST), (rv / NST) & 1)) break;
-                if (j == nmax - 1 && sq.lk - j * AT < AT)
-                    zero_tail_rows<D>(sb + S::RING + (rv % NST) * TILE, sq.lk - j * AT, lane);
-                for (int w = 0; w < 2 && ok; ++w) {
-                    if (j >= nt[w]) continue;
-                    const uint64_t b = vd + (rv % NST) * (TILE >> 4);
-                    for (int hf = 0; hf < 2; ++hf) {
-                        if (!wait(pready0 + 8 * (2 * w + hf), j & 1)) break;
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc_mma_ss_warp(tmem + 128 * w, desc(khi, klo + ((w * TILE) >> 4) + kstep_k(ks)),
+                                       desc(khi, b + kstep_k(ks)), id_s, ks > 0);
+                    tc_commit_warp(sfull0 + 8 * w);
+                };
 #pragma unroll
-                        for (int k = 0; k < AT / 32; ++k) {
-                            const int ks = 4 * hf + k;
-                            tc_mma_ts_warp(tmem + TM_O + D * w, tmem + 128 * w + 8 * ks, b + kstep_mn(ks), id_o,
-                                           j > 0 || ks > 0);
+                for (int w = w0; w < w1; ++w)
+                    if (nt[w] > 0 && wait(qfull0 + 8 * w, 0)) score(w, 0);
+                if (nmax > 0) release(0);
+                for (int j = 0; j < nmax && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+                    const int st = (2 * j + 1) % NST;
+#pragma unroll
+                    for (int w = w0; w < w1; ++w) {
+                        if (!ok || j >= nt[w]) continue;
+                        if (kOwnP && j + 1 < nt[w] && wait(sfree0 + 8 * w, j & 1)) score(w, j + 1);
+                        if (!ok || !arrived(2 * j + 1)) continue;
+                        if (sq.lk - j * AT < AT) zero_tail_rows<D>(sb + S::RING + st * TILE, sq.lk - j * AT, lane);
+                        const uint32_t b = mlo + ((S::RING + st * TILE) >> 4);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (!wait(pready0 + 8 * (2 * w + hf), j & 1)) break;
+#pragma unroll
+                            for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
+                                tc_mma_ts_warp(tmem + TM_O + D * w, tmem + TM_P + TM_PSTEP * w + 8 * ks,
+                                               desc(mhi, b + kstep_mn(ks)), id_o, j > 0 || ks > 0);
                         }
+                        if (!ok) continue;
+                        if (kOwnP || j + 1 == nt[w]) tc_commit_warp(odone0 + 8 * w);
+                        if (!kOwnP && j + 1 < nt[w]) score(w, j + 1);
                     }
                     if (!ok) break;
-                    if (j + 1 < nt[w]) {
-                        if (!wait(full0 + 8 * (rk % NST), (rk / NST) & 1)) break;
-                        score(w, rk);
-                    } else {
-                        tc_commit_warp(odone0 + 8 * w);
-                    }
+                    // (a tile with fewer key tiles than the other lets theirs go as well)
+                    release(2 * j + 1);
+                    if (j + 1 < nmax) release(2 * j + 2);
                 }
-                if (!ok) break;
-                tc_commit_warp(empty0 + 8 * (rv % NST));
-                if (j + 1 < nmax) tc_commit_warp(empty0 + 8 * (rk % NST));
-            }
-            if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
+                if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
+            };
+            using I0 = std::integral_constant<int, 0>;
+            using I1 = std::integral_constant<int, 1>;
+            using I2 = std::integral_constant<int, 2>;
+            if constexpr (kIssuers == 1) issue(I0{}, I2{});
+            else if (warp == 8) issue(I0{}, I1{});
+            else issue(I1{}, I2{});
         }
     }
     tc_fence_before();
