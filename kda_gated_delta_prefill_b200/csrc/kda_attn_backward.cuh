@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         bool ok = true;
         for (int it = 0; it < total; ++it) {
             const int i = first + it % cnt, st = it % NST;
-            ok = mbar_wait_spin(qfull + 8 * st, (it / NST) & 1) && mbar_wait_spin(sfull, it & 1);
+            ok = mbar_wait_quiet(qfull + 8 * st, (it / NST) & 1) && mbar_wait_quiet(sfull, it & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(pready);
 
-            ok = __all_sync(0xffffffffu, mbar_wait_spin(dpfull, it & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, it & 1));
             if (!ok) break;
             tc_fence_after();
             tc_ld32(td, r[0]);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(dsready);
         }
-        if (ok && total > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(done, 0));
+        if (ok && total > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             const int tail = sq.lq - (nq - 1) * AT;  // rows of the last query tile
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_quiet(bar, parity));
                 tc_fence_after();
                 return ok;
             };
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
             const uint32_t ts = tmem + lb + TM_S + 128 * (j & 1) + 64 * half;
-            ok = __all_sync(0xffffffffu, mbar_wait_spin(sfull0 + 8 * (j & 1), (j >> 1) & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(sfull0 + 8 * (j & 1), (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
             uint32_t x[2][32];
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 }
                 pr[e] = a;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait_spin(dpfull, j & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, j & 1));
             if (!ok) break;
             tc_fence_after();
             tc_ld32(td, x[0]);
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(dsready);
         }
-        if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_spin(done, 0));
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else if (half == 0) {
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             const int tail = sq.lk - (nt - 1) * AT;  // rows of the last key tile, if fewer than 128
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(bar, parity));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_quiet(bar, parity));
                 tc_fence_after();
                 return ok;
             };
