@@ -581,13 +581,13 @@ def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None
     key/value head.  dout's rows may be strided like q's.  Rows of no sequence are not written.
     """
     import torch
+    if q.dim() != 4 or dout.shape != q.shape:
+        raise ValueError("q must be [B,T,H,D], dout like it, k and v [B,Tk,HKV,D]")
     B, T, H, D = q.shape
     rows, dims, dev = _attention_inputs(
         q, k, v, cu_seqlens, cu_seqlens_k,
         (("o", o, torch.bfloat16, B * T * H * D, True), ("lse", lse, torch.float32, B * H * T, True),
          ("dout", dout, torch.bfloat16, None, False), ("workspace", workspace, torch.uint8, None, True)))
-    if dout.shape != q.shape:
-        raise ValueError("dout must be [B,T,H,D]")
     dq = torch.empty(B, T, H, D, dtype=torch.bfloat16, device=dev)
     dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     dv = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)

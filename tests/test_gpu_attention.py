@@ -151,3 +151,178 @@ def test_backward_matches_the_formula(B, T, Tk, H, HKV, D, lens, klens):
             assert (grads[0][b, a:a + n] == 0).all()
         if n == 0:
             assert (grads[1][b, c:c + m] == 0).all() and (grads[2][b, c:c + m] == 0).all()
+
+
+def run(q, k, v, dout, cu=None, cu_k=None, **kw):
+    o, lse = kda.attention_forward(q, k, v, cu, cu_k, **kw)
+    return (o, lse, *kda.attention_backward(q, k, v, o, lse, dout, cu, cu_k, **kw))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_of_packed_qkv_and_strided_dout(D):
+    """Views of one packed tensor give the same bits as compact tensors."""
+    B, T, H, HKV = 2, 300, 4, 2
+    qkv = heads(5, B, T, H + 2 * HKV, D)
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:H + HKV], qkv[:, :, H + HKV:]
+    wide = heads(6, B, T, 2 * H, D)
+    dout = wide[:, :, H:]
+    got = run(q, k, v, dout)
+    want = run(q.contiguous(), k.contiguous(), v.contiguous(), dout.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    check_forward(q, k, v, got[0], got[1])
+    check_backward(q, k, v, dout, got[2:])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_of_no_sequence(D):
+    """Rows before, between and behind the sequences hold NaN and infinities: outputs there stay as they were, and
+    nothing of them reaches a result; a workspace of NaN does not either."""
+    lens, klens, H, HKV = [70, 0, 200], [100, 30, 150], 4, 2
+    pad_q, pad_k = 90, 60
+    T, TK = sum(lens) + pad_q, sum(klens) + pad_k
+    q, k, v, dout = heads(1, 1, T, H, D), heads(2, 1, TK, HKV, D), heads(3, 1, TK, HKV, D), heads(4, 1, T, H, D)
+    for x, n in ((q, sum(lens)), (k, sum(klens)), (v, sum(klens)), (dout, sum(lens))):
+        x[:, n:] = math.nan
+        x[:, n::2] = math.inf
+    cu, cu_k = cu_of(lens), cu_of(klens)
+    o = torch.full((1, T, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, H, T), 7.0, device="cuda")
+    kda.attention_forward(q, k, v, cu, cu_k, o=o, lse=lse)
+    n = sum(lens)
+    assert (o[:, n:] == 7).all() and (lse[:, :, n:] == 7).all()
+    check_forward(q, k, v, o, lse, lens, klens)
+    ws = torch.full((kda.attention_backward_workspace_size(1, T, H, 3),), 0xff, dtype=torch.uint8, device="cuda")
+    o[:, n:] = math.nan
+    grads = kda.attention_backward(q, k, v, o, lse, dout, cu, cu_k, workspace=ws)
+    torch.cuda.synchronize()
+    assert kda.device_error() == 0
+    check_backward(q, k, v, dout, grads, lens, klens)
+    # offsets past the tensors are cut off at them
+    far = cu.clone()
+    far[-1] += 10000
+    o2, lse2 = kda.attention_forward(q[:, :n], k, v, far, cu_k)
+    assert torch.equal(o2, o[:, :n]) and torch.equal(lse2, lse[:, :, :n])
+
+
+@pytest.mark.parametrize("D,scale", [(64, 0.5), (128, 3.0), (128, 1e-6), (64, 1.0)])
+def test_scores_far_apart(D, scale):
+    """Maxima that grow by hundreds from key tile to key tile, and scores hundreds below them.  Scores of up to S are
+    off by about S * 128 * 2^-24 here, which weighs p and lse: the bounds grow with it."""
+    T, H = 700, 2
+    q, k, v = heads(1, 1, T, H, D), heads(2, 1, T, H, D), heads(3, 1, T, H, D)
+    k *= torch.linspace(0.1, 12, T, device="cuda")[None, :, None, None]
+    k[:, 130:260] *= -1
+    k = k.bfloat16()
+    o, lse = kda.attention_forward(q, k, v, scale=scale)
+    f = formula(q[0], k[0], v[0], scale)
+    top = float((q[0].double().abs().transpose(0, 1) @ k[0].double().abs().permute(1, 2, 0)).max()) * scale
+    slack = 2 * (FP32 + top * 2.0 ** -19)
+    assert ((lse[0].double() - f["lse"]).abs() <= slack).all()
+    tol = (HALF + slack) * f["o_w"] + HALF * f["o"].abs() + slack * 8 * v.abs().max().double()
+    assert ((o[0].double() - f["o"]).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_against_differences(D):
+    """The directional derivative of sum(o * dout) by central differences of the formula in 64 bits."""
+    T, H, HKV, e = 150, 4, 2, 1e-5
+    q, k, v, dout = heads(1, 1, T, H, D), heads(2, 1, T, HKV, D), heads(3, 1, T, HKV, D), heads(4, 1, T, H, D)
+    grads = run(q, k, v, dout)[2:]
+    loss = lambda *x: (formula(*(y[0] for y in x), D ** -0.5)["o"] * dout[0].double()).sum()  # noqa: E731
+    x = [q.double(), k.double(), v.double()]
+    f = formula(q[0], k[0], v[0], D ** -0.5, dout[0])
+    for i, name in enumerate(("dq", "dk", "dv")):
+        u = torch.randn(x[i].shape, generator=torch.Generator("cuda").manual_seed(i), device="cuda", dtype=torch.float64)
+        step = lambda s: loss(*(y + s * e * u if j == i else y for j, y in enumerate(x)))  # noqa: E731
+        want = (step(1) - step(-1)) / (2 * e)
+        got = (grads[i].double() * u).sum()
+        tol = (((HALF + FP32) * f[name + "_w"] + HALF * f[name].abs()) * u[0].abs()).sum()  # every rounding the same way
+        assert (got - want).abs() <= tol and tol < 0.5 * (grads[i].double() * u).abs().sum()
+
+
+def test_same_bits_on_every_run_and_stream():
+    q, k, v, dout = heads(1, 1, 2000, 8, 128), heads(2, 1, 2000, 2, 128), heads(3, 1, 2000, 2, 128), heads(4, 1, 2000, 8, 128)
+    cu = cu_of([700, 1, 1299])
+    want = run(q, k, v, dout, cu)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for s in streams:  # at the same time, each with its own workspace; once by argument, else by the current stream
+        with torch.cuda.stream(s):
+            got.append(run(q, k, v, dout, cu) if s is not streams[0] else None)
+    got[0] = run(q, k, v, dout, cu, stream=streams[0])
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_captured_forward_and_backward_follow_new_inputs_and_lengths():
+    """A graph of the pass replays on new values and new offsets of the same tensors."""
+    T, H, HKV, D = 600, 4, 1, 128
+    q, k, v, dout = (torch.empty(1, T, h, D, dtype=torch.bfloat16, device="cuda") for h in (H, HKV, HKV, H))
+    cu = cu_of([100, 500])
+
+    def fill(seed, lens):
+        for i, x in enumerate((q, k, v, dout)):
+            x.copy_(heads(seed + i, *x.shape))
+        cu.copy_(cu_of(lens))
+
+    fill(1, [100, 500])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(q, k, v, dout, cu)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(q, k, v, dout, cu)
+    for seed, lens in ((10, [333, 267]), (20, [1, 599]), (30, [600, 0])):
+        fill(seed, lens)
+        g.replay()
+        torch.cuda.synchronize()
+        check_forward(q, k, v, out[0], out[1], lens)
+        check_backward(q, k, v, dout, out[2:], lens)
+    assert kda.device_error() == 0
+
+
+def test_many_sequences():
+    """More sequences than a search step covers, of every length from zero up."""
+    lens = [i % 37 for i in range(1500)]
+    T = sum(lens)
+    q, k, v, dout = heads(1, 1, T, 2, 64), heads(2, 1, T, 1, 64), heads(3, 1, T, 1, 64), heads(4, 1, T, 2, 64)
+    out = run(q, k, v, dout, cu_of(lens))
+    torch.cuda.synchronize()
+    some = [i for i in range(1500) if i % 97 in (0, 1, 2)]
+    for i in some:
+        a, n = sum(lens[:i]), lens[i]
+        check_forward(q[:, a:a + n], k[:, a:a + n], v[:, a:a + n], out[0][:, a:a + n], out[1][:, :, a:a + n])
+        check_backward(q[:, a:a + n], k[:, a:a + n], v[:, a:a + n], dout[:, a:a + n],
+                       [out[2][:, a:a + n], out[3][:, a:a + n], out[4][:, a:a + n]])
+    assert kda.device_error() == 0
+
+
+def test_no_queries_or_no_keys():
+    q, k = heads(1, 2, 50, 4, 64), heads(2, 2, 30, 2, 64)
+    none_k, none_q = k[:, :0], q[:, :0]
+    o, lse = kda.attention_forward(q, none_k, none_k)
+    assert (o == 0).all() and (lse == -math.inf).all()
+    dq, dk, dv = kda.attention_backward(q, none_k, none_k, o, lse, q)
+    assert (dq == 0).all() and dk.numel() == 0
+    o, lse = kda.attention_forward(none_q, k, k)
+    assert o.numel() == 0
+    dq, dk, dv = kda.attention_backward(none_q, k, k, o, lse, none_q)
+    assert (dk == 0).all() and (dv == 0).all()
+    torch.cuda.synchronize()
+    assert kda.device_error() == 0
+
+
+def test_split_keys_join_by_lse():
+    """The first query's attention over the prefix and over its own key, joined by their lse, is its attention over both."""
+    n, m, D = 200, 500, 128
+    q, k, v = heads(1, 1, n, 2, D), heads(2, 1, m, 2, D), heads(3, 1, m, 2, D)
+    oa, la = kda.attention_forward(q[:, :1], k[:, :m - n], v[:, :m - n])
+    ob, lb = kda.attention_forward(q[:, :1], k[:, m - n:m - n + 1], v[:, m - n:m - n + 1])
+    w = torch.softmax(torch.stack([la, lb]), 0)[..., None]
+    both = (w[0] * oa[0].transpose(0, 1) + w[1] * ob[0].transpose(0, 1)).float()
+    f = formula(q[0], k[0], v[0], D ** -0.5)
+    assert (both[0, :, 0].double() - f["o"][0]).abs().max() <= (4 * HALF * f["o_w"][0]).max()

@@ -4,6 +4,11 @@ Tables, slots, scales and codes are compared exactly with plain loops.  Attentio
 bits: the softmax's weights are fp16 (half a step is 2^-11, weighted by |v|), the result is rounded to bf16 (2^-8), and
 the fp32 steps add less than 2^-12 of the same weights, as in test_gpu_attention.py; queries are exact in fp16 but for
 elements 2^-14 below a row's largest, which round at 2^-24 of it.
+
+Weights below fp16's normal range are off by half of its smallest step, 2^-25, instead of by a relative error.  A weight is
+C p_j vs_j (probability times value scale), with C such that the largest is at least 2^12, so C >= 2^12 / max_j p_j vs_j,
+and sum_j C p_j vs_j code_j is divided by C.  The result is then off by at most
+2^-25 sum_j |code_j| / C <= 2^-37 sum_j |code_j| max_j p_j vs_j.
 """
 import math
 
@@ -254,7 +259,7 @@ def formula(q, kc, vc, ks, vs, table, lens, scale):
     B, H, D = q.shape
     HKV, bs = kc.shape[1], kc.shape[2]
     o = torch.zeros(B, H, D, dtype=torch.float64, device="cuda")
-    w = torch.zeros_like(o)
+    w, tiny = torch.zeros_like(o), torch.zeros_like(o)
     lse = torch.full((B, H), -math.inf, dtype=torch.float64, device="cuda")
     for b, n in enumerate(lens):
         if n <= 0:
@@ -268,7 +273,10 @@ def formula(q, kc, vc, ks, vs, table, lens, scale):
         o[b] = torch.einsum("hgn,hnd->hgd", p, v).reshape(H, D)
         w[b] = torch.einsum("hgn,hnd->hgd", p, v.abs()).reshape(H, D)
         lse[b] = z.reshape(H)
-    return o, lse, w
+        scales = vs[ids].double().repeat_interleave(bs, 0)[:n].T[:, None]  # [HKV, 1, n]
+        codes = (v.abs() / torch.where(scales == 0, 1.0, scales).transpose(1, 2)).sum(1)
+        tiny[b] = (2.0 ** -37 * (p * scales).amax(2)[..., None] * codes[:, None]).reshape(H, D)
+    return o, lse, w, tiny
 
 
 def make_decode(dtype, lens, H, HKV, D, bs, seed, width=None):
@@ -294,10 +302,10 @@ def make_decode(dtype, lens, H, HKV, D, bs, seed, width=None):
 
 def check_decode(args, lens, o, lse, scale=None):
     q = args[0]
-    f, z, w = formula(*args, lens, q.shape[2] ** -0.5 if scale is None else scale)
+    f, z, w, tiny = formula(*args, lens, q.shape[2] ** -0.5 if scale is None else scale)
     empty = torch.tensor([n <= 0 for n in lens], device="cuda")
     assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
-    tol = (FP16 + FP32) * w + BF16 * f.abs() + 1e-30
+    tol = (FP16 + FP32) * w + BF16 * f.abs() + tiny + 1e-30
     ratio = ((o.double() - f).abs() / tol)[~empty]
     assert ratio.numel() == 0 or ratio.max() <= 1, float(ratio.max())
     dz = (lse.double() - z)[~empty].abs()
@@ -329,3 +337,149 @@ def test_decode_matches_the_formula(dtype, lens, H, HKV, D, bs):
     torch.cuda.synchronize()
     assert kda.device_error() == 0
     check_decode(args, lens, o, lse)
+
+
+def test_decode_rows_of_packed_qkv_scale_and_given_buffers():
+    lens, H, HKV, D = [300, 17, 0, 64], 8, 2, 128
+    args = make_decode(E4M3, lens, H, HKV, D, 64, 3)
+    packed = torch.zeros(4, (H + 2 * HKV) * D, dtype=torch.bfloat16, device="cuda")
+    q = packed[:, :H * D].view(4, H, D)
+    q.copy_(args[0])
+    o = torch.full((4, H, D), math.nan, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, H), math.nan, device="cuda")
+    ws = torch.full((kda.attention_decode_workspace_size(4, H, HKV, D, args[5].shape[1], 64),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    wide = torch.full((4, 40), 1 << 30, dtype=torch.int32, device="cuda")  # a table row inside a wider one
+    wide[:, 3:3 + args[5].shape[1]] = args[5]
+    table = wide[:, 3:3 + args[5].shape[1]]
+    kda.attention_decode(q, *args[1:5], table, i32(lens), scale=0.3, o=o, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    check_decode(args, lens, o, lse, scale=0.3)
+    again = kda.attention_decode(args[0], *args[1:], i32(lens), scale=0.3)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+def test_decode_with_scales_far_apart(dtype):
+    """Value scales 2^40 apart between blocks (weights ride on their exponents), key scales that make scores of hundreds, and a
+    block whose value scale is zero.  Scores of up to S are off by S * 2^-20 or so, which weighs p and lse."""
+    lens, H, HKV, D, bs = [900, 40], 8, 2, 128, 16
+    q, kc, vc, ks, vs, table = make_decode(dtype, lens, H, HKV, D, bs, 9)
+    g = torch.Generator("cuda").manual_seed(1)
+    vs.copy_(torch.exp2(torch.randint(-40, 1, vs.shape, generator=g, device="cuda").float()))
+    ks.mul_(torch.exp2(torch.randint(-6, 5, ks.shape, generator=g, device="cuda").float()))
+    vs[table[0, 3].long()] = 0
+    args = (q, kc, vc, ks, vs, table)
+    o, lse = kda.attention_decode(*args, i32(lens))
+    f, z, w, tiny = formula(*args, lens, D ** -0.5)
+    s_max = 0.0
+    for b, n in enumerate(lens):
+        ids = table[b, :-(-n // bs)].long()
+        k = (kc.view(torch.uint8)[ids].view(dtype).double() * ks[ids].double()[..., None, None]).nan_to_num()
+        s_max = max(s_max, float((q[b].double().abs().view(HKV, -1, D)[None] @ k.abs().transpose(2, 3)).max()) * D ** -0.5)
+    slack = 2 * (FP32 + s_max * 2.0 ** -19)
+    assert ((lse.double() - z).abs() <= slack).all()
+    assert ((o.double() - f).abs() <= (FP16 + slack) * w + BF16 * f.abs() + tiny).all()
+
+
+def test_decode_blocks_out_of_range_and_lengths_past_the_table():
+    lens, H, HKV, D, bs = [100, 50], 4, 2, 64, 16
+    args = make_decode(INT8, lens, H, HKV, D, bs, 4)
+    bad = args[5].clone()
+    bad[0, 2], bad[0, 5] = args[1].shape[0], -3       # tokens 32..47 and 80..95 do not count
+    o, lse = kda.attention_decode(*args[:5], bad, i32(lens))
+    assert kda.device_error() == 16
+    keep = [i for i in range(100) if i // bs not in (2, 5)]
+    ids = args[5][0].long()
+    k, v = ((c[ids].double() * s[ids].double()[..., None, None]).transpose(1, 2).reshape(-1, HKV, D)[keep]
+            for c, s in ((args[1], args[3]), (args[2], args[4])))
+    x = torch.einsum("hgd,nhd->hgn", args[0][0].double().view(HKV, 2, D), k) * D ** -0.5
+    want = torch.einsum("hgn,nhd->hgd", torch.softmax(x, 2), v).reshape(H, D)
+    weight = torch.einsum("hgn,nhd->hgd", torch.softmax(x, 2), v.abs()).reshape(H, D)
+    assert ((o[0].double() - want).abs() <= (FP16 + FP32) * weight + BF16 * want.abs()).all()
+    check_decode(tuple(a[1:] if i in (0, 5) else a for i, a in enumerate(args)), lens[1:], o[1:], lse[1:])
+    none = torch.full_like(bad, -1)
+    o, lse = kda.attention_decode(*args[:5], none, i32(lens))
+    assert (o == 0).all() and (lse == -math.inf).all() and kda.device_error() == 16
+    o, lse = kda.attention_decode(*args, i32([1000, 50]))  # row 0 is as long as its table
+    assert kda.device_error() == 16
+    full = bs * args[5].shape[1]
+    check_decode(args, [full, 50], *kda.attention_decode(*args, i32([full, 50])))
+    assert torch.equal(o[0], kda.attention_decode(*args, i32([full, 50]))[0][0]) and kda.device_error() == 0
+
+
+def test_decode_same_bits_on_every_run_and_stream():
+    lens = [3000, 1, 700, 0, 64, 1500]
+    args = make_decode(E4M3, lens, 16, 4, 128, 32, 8)
+    n = i32(lens)
+    want = kda.attention_decode(*args, n)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(kda.attention_decode(*args, n))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("D,bs", [(128, 64), (64, 16)])
+def test_a_server_s_steps(dtype, D, bs):
+    """Prompts through plan, attention, append; then captured steps of plan, append and decode, replayed while the requests
+    grow: every step's attention is the formula's over what the cache holds, and the cache holds what plain loops store."""
+    H, HKV, rows, width, blocks = 8, 2, 5, 20, 60
+    g = torch.Generator("cuda").manual_seed(3)
+    free = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32)
+    kc, vc = (torch.zeros(blocks, HKV, bs, D, dtype=torch.int8, device="cuda").view(dtype) for _ in range(2))
+    ks, vs = (torch.zeros(blocks, HKV, device="cuda") for _ in range(2))
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    prompt = [37, 1, 130, 0, 64]
+    T = sum(prompt)
+    qkv = torch.randn(1, T, H + 2 * HKV, D, generator=g, device="cuda").bfloat16()
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:H + HKV], qkv[:, :, H + HKV:]
+    cu, lens, slots, used = kda.cache_plan(i32([0] * rows), i32(prompt), table, free, bs, T)
+    o, lse = kda.attention_forward(q, k, v, cu)
+    kda.cache_append(k[0], v[0], kc, vc, ks, vs, slots)
+    plain = [x.cpu().clone() for x in (torch.zeros_like(kc.view(torch.int8)).view(dtype),) * 2] + [torch.zeros(blocks, HKV)] * 2
+    plain = [p.clone() for p in plain]
+    plain_append(k[0].cpu(), plain[0], plain[2], slots.tolist())
+    plain_append(v[0].cpu(), plain[1], plain[3], slots.tolist())
+
+    ctx, one = lens.clone(), i32([1, 1, 1, 1, 0])  # the last request waits
+    free_now = free.roll(-int(used.item())).contiguous()
+    step_qkv = torch.zeros(4, H + 2 * HKV, D, dtype=torch.bfloat16, device="cuda")
+    q_all = torch.zeros(rows, H, D, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        _, n, slot, took = kda.cache_plan(ctx, one, table, free_now, bs, 4)
+        kda.cache_append(step_qkv[:, H:H + HKV], step_qkv[:, H + HKV:], kc, vc, ks, vs, slot)
+        return (*kda.attention_decode(q_all, kc, vc, ks, vs, table, n), n, slot, took)
+
+    state = [x.clone() for x in (kc.view(torch.uint8), vc.view(torch.uint8), ks, vs, table)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for x, y in zip((kc.view(torch.uint8), vc.view(torch.uint8), ks, vs, table), state):  # as before the trial run
+        x.copy_(y)
+    for i in range(40):
+        step_qkv.copy_(torch.randn(step_qkv.shape, generator=g, device="cuda") * (1 + i / 4))
+        q_all.copy_(torch.randn(q_all.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        o, lse, n, slot, took = out
+        plain_append(step_qkv[:, H:H + HKV].cpu(), plain[0], plain[2], slot.tolist())
+        plain_append(step_qkv[:, H + HKV:].cpu(), plain[1], plain[3], slot.tolist())
+        check_decode((q_all, kc, vc, ks, vs, table), n.tolist(), o, lse)
+        ctx.copy_(n)
+        free_now.copy_(free_now.roll(-int(took.item())))
+    assert n.tolist() == [77, 41, 170, 40, 64] and kda.device_error() == 0
+    real = sorted({b for r, m in zip(table.tolist(), n.tolist()) for b in r[:-(-m // bs)]})
+    assert len(real) == sum(-(-m // bs) for m in n.tolist())  # no block twice
+    for got, want in zip((kc, vc, ks, vs), plain):
+        assert torch.equal(bits(got)[real], bits(want)[real])
