@@ -135,6 +135,22 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
                     : launch(kda_attn_fwd_kernel<64>, AttnFwdSmem<64>::TOTAL);
 }
 
+namespace {
+
+// CTAs (a cluster) that share the query heads of a key tile: as long as they fill the SMs in one wave.  With fewer CTAs than
+// SMs a key tile's loop over all heads of its group is the longest chain there is; with more than a wave of them the clusters
+// cost more than they balance (D = 128, 32/8 heads; us per backward with 1, 2 and 4 CTAs):
+//   512 tokens (32 key tiles): 41, 33, 32    1,024 (64): 69, 52, 60    2,048 (128): 133, 140, 161
+// and 8/1 heads, 2,048 tokens (16 key tiles): 232, 131, 72 and, with 8, 47.
+int backward_split(int group, int64_t units, int sms)
+{
+    int split = 1;
+    while (split < 8 && group % (2 * split) == 0 && 2 * split * units <= sms) split *= 2;
+    return split;
+}
+
+}  // namespace
+
 extern "C" size_t kda_attention_backward_workspace_size(int B, int T, int H, int num_seqs)
 {
     if (B <= 0 || T < 0 || H <= 0 || num_seqs < 0 || (num_seqs > 0 && B != 1)) return 0;
@@ -201,15 +217,41 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     // a side without rows: the kernels write zeros to the other side's gradients and load nothing
     if (!d.rows) mq = mdo = mk;
     if (!d.krows) mk = mv = mq;
+    p.split = backward_split(H / HKV, static_cast<int64_t>(p.kslots) * HKV, info.sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto run = [&](auto stats, auto dkv, int dkv_smem, auto dqk, int dq_smem) {
-        if (cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem) != cudaSuccess ||
-            cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem) != cudaSuccess)
+    // dK/dV is set up while the statistics are formed, and dQ fills the SMs that dK/dV leaves idle at its end
+    auto launch = [&](auto kern, int64_t grid, int smem, int cluster, bool early) {
+        if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return KDA_ERR_CUDA;
-        if (d.rows) stats<<<p.qslots * H, kAttnStatThreads, 0, s>>>(p);
-        if (d.krows) dkv<<<p.kslots * HKV, kAttnBwdThreads, dkv_smem, s>>>(p, mq, mk, mv, mdo);
-        if (d.rows) dqk<<<p.qslots * H, kAttnBwdThreads, dq_smem, s>>>(p, mq, mk, mv, mdo);
-        return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(kAttnBwdThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2]{};
+        cfg.attrs = attr;
+        if (early) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+        }
+        if (cluster > 1) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            attr[cfg.numAttrs].val.clusterDim.x = cluster;
+            attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+            ++cfg.numAttrs;
+        }
+        return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, mdo) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    };
+    auto run = [&](auto stats, auto dkv, int dkv_smem, auto dqk, int dq_smem) {
+        kda_status_t r = KDA_OK;
+        if (d.rows) {
+            stats<<<p.qslots * H, kAttnStatThreads, 0, s>>>(p);
+            if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        }
+        if (d.krows) r = launch(dkv, static_cast<int64_t>(p.kslots) * HKV * p.split, dkv_smem, p.split, d.rows > 0);
+        if (r == KDA_OK && d.rows) r = launch(dqk, static_cast<int64_t>(p.qslots) * H, dq_smem, 1, d.krows > 0);
+        return r;
     };
     return D == 128 ? run(kda_attn_stats_kernel<128>, kda_attn_dkv_kernel<128>, AttnDkvSmem<128>::TOTAL,
                           kda_attn_dq_kernel<128>, AttnDqSmem<128>::TOTAL)

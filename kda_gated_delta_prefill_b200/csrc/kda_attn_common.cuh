@@ -78,6 +78,23 @@ __device__ __forceinline__ void zero_tail_rows(uint32_t tile, int first, int lan
     __syncwarp();
 }
 
+// Thread-block clusters: a barrier of all their threads, and four floats of CTA `rank`'s shared memory.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t saddr, int rank)
+{
+    float4 v;
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+        " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(saddr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // The sequences of a batch: packed (cu given, clamped to the tensors' rows) or plain.
 struct SeqView {
     const int32_t *cu_q, *cu_k;  // [N+1], null for a plain batch
