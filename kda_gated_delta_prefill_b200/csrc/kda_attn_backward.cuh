@@ -88,8 +88,9 @@ struct AttnDkvSmem {
     static constexpr int Q = 2 * TILE;              // K, V, then the rings of Q, dO and statistics
     static constexpr int DO = Q + NST * TILE;
     static constexpr int STAT = DO + NST * TILE;
-    static constexpr int BAR = STAT + NST * 1024;   // qfull qempty dofull doempty [NST], kfull vfull sfull pready dpfull dsready done
-    static constexpr int TMEM_SLOT = BAR + (4 * NST + 7) * 8;
+    // qfull qempty dofull doempty [NST], kfull vfull sfull pready dpfull dsready done sfree dpfree
+    static constexpr int BAR = STAT + NST * 1024;
+    static constexpr int TMEM_SLOT = BAR + (4 * NST + 9) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -105,7 +106,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 {
     using S = AttnDkvSmem<D>;
     constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
+    constexpr bool kOwn = D == 64;  // P and dS have columns of their own, in halves like those of S and dP
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
+    constexpr uint32_t TM_P = kOwn ? 384 : TM_S, TM_DS = kOwn ? 448 : TM_DP, TM_HALF = kOwn ? 32 : 64;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -122,13 +125,12 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 
     const uint32_t qfull = sb + S::BAR, qempty = qfull + 8 * NST, dofull = qempty + 8 * NST, doempty = dofull + 8 * NST,
                    kfull = doempty + 8 * NST, vfull = kfull + 8, sfull = kfull + 16, pready = kfull + 24,
-                   dpfull = kfull + 32, dsready = kfull + 40, done = kfull + 48;
+                   dpfull = kfull + 32, dsready = kfull + 40, done = kfull + 48, sfree = kfull + 56, dpfree = kfull + 64;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
         for (int s = 0; s < 4 * NST; ++s) mbar_init(qfull + 8 * s, 1);
         for (uint32_t b : {kfull, vfull, sfull, dpfull, done}) mbar_init(b, 1);
-        mbar_init(pready, 8);
-        mbar_init(dsready, 8);
+        for (uint32_t b : {pready, dsready, sfree, dpfree}) mbar_init(b, 8);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -148,6 +150,17 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const int half = warp >> 2, quarter = warp & 3;
         const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
         const uint32_t ts = tmem + lb + TM_S + 64 * half, td = tmem + lb + TM_DP + 64 * half;
+        const uint32_t tp = tmem + lb + TM_P + TM_HALF * half, tds = tmem + lb + TM_DS + TM_HALF * half;
+        auto arrive = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        // the MMAs of iteration it - 1 that read P (or dS) are done with it
+        auto reusable = [&](uint32_t bars, int it) {
+            if (!kOwn || it == 0) return true;
+            return __all_sync(0xffffffffu, mbar_wait_quiet(bars + 8 * ((it - 1) % NST), ((it - 1) / NST) & 1)) != 0;
+        };
         const int key = j0 + 32 * quarter + lane;
         const float c = p.scale_log2;
         bool ok = true;
@@ -163,6 +176,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             const float4 *l2 = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 16 * half;
             const float4 *dl = l2 + 32;
             tc_wait_ld();
+            if (kOwn) arrive(sfree);
             // queries q >= key - diff see the key
             const int from = key - diff - i * AT - 64 * half;
             const bool cut = __any_sync(0xffffffffu, from > 0);
@@ -186,17 +200,17 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 pr[2 * e] = a;
                 pr[2 * e + 1] = b;
             }
+            ok = reusable(doempty, it);
+            if (!ok) break;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16(pr[16 * k + e].x, pr[16 * k + e].y);
-                tc_st16(ts + 16 * k, w);
+                tc_st16(tp + 16 * k, w);
             }
             tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pready);
+            arrive(pready);
 
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, it & 1));
             if (!ok) break;
@@ -204,6 +218,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             tc_ld32(td, r[0]);
             tc_ld32(td + 32, r[1]);
             tc_wait_ld();
+            if (kOwn) arrive(dpfree);
+            ok = reusable(qempty, it);
+            if (!ok) break;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t w[16];
@@ -220,12 +237,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                     w[2 * e] = pack_bf16(a.x, a.y);
                     w[2 * e + 1] = pack_bf16(b.x, b.y);
                 }
-                tc_st16(td + 16 * k, w);
+                tc_st16(tds + 16 * k, w);
             }
             tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dsready);
+            arrive(dsready);
         }
         if (ok && total > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
         if (!ok) {
@@ -305,10 +320,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             }
         } else if (warp == 8 && total > 0) {
             // ---------------- MMAs ----------------
-            const uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
-            const uint64_t kd = tile_desc_k(sb), vd = tile_desc_k(sb + TILE);
-            const uint64_t qk = tile_desc_k(sb + S::Q), dok = tile_desc_k(sb + S::DO);
-            const uint64_t qm = tile_desc_mn(sb + S::Q), dom = tile_desc_mn(sb + S::DO);
+            constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
+            const TileDesc desc(sb);
             const int tail = sq.lq - (nq - 1) * AT;  // rows of the last query tile
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -316,42 +329,39 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            auto score = [&](int it) {  // S^T = K Q^T
-                const int st = it % NST;
-                if (!wait(qfull + 8 * st, (it / NST) & 1)) return;
-                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + S::Q + st * TILE, tail, lane);
+            // D[128 keys][128 queries] = (K or V) (Q or dO)^T of iteration it, once the tile is there
+            auto product = [&](uint32_t d, int keys, int ring, uint32_t full, uint32_t commit, int it) {
+                const int st = it % NST, at = ring + st * TILE;
+                if (!wait(full + 8 * st, (it / NST) & 1)) return;
+                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + at, tail, lane);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss_warp(tmem + TM_S, kd + kstep_k(ks), qk + st * (TILE >> 4) + kstep_k(ks), id_s, ks > 0);
-                tc_commit_warp(sfull);
+                    tc_mma_ss_warp(d, desc.k(keys, ks), desc.k(at, ks), id_s, ks > 0);
+                tc_commit_warp(commit);
             };
-            auto dprob = [&](int it) {  // dP^T = V dO^T
-                const int st = it % NST;
-                if (!wait(dofull + 8 * st, (it / NST) & 1)) return;
-                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + S::DO + st * TILE, tail, lane);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss_warp(tmem + TM_DP, vd + kstep_k(ks), dok + st * (TILE >> 4) + kstep_k(ks), id_s, ks > 0);
-                tc_commit_warp(dpfull);
-            };
-            // D += A B with A's halves of 64 columns (32 words) at a and a + 64
-            auto accumulate = [&](uint32_t d, uint32_t a, uint64_t b, bool more) {
+            auto score = [&](int it) { product(tmem + TM_S, 0, S::Q, qfull, sfull, it); };
+            auto dprob = [&](int it) { product(tmem + TM_DP, TILE, S::DO, dofull, dpfull, it); };
+            // D += A B, A in two halves of 64 queries
+            auto accumulate = [&](uint32_t d, uint32_t a, int at, bool more) {
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
-                    tc_mma_ts_warp(d, a + (ks >> 2) * 64 + (ks & 3) * 8, b + kstep_mn(ks), id_d, more || ks > 0);
+                    tc_mma_ts_warp(d, a + (ks >> 2) * TM_HALF + (ks & 3) * 8, desc.mn(at, ks), id_d, more || ks > 0);
             };
             if (wait(kfull, 0)) score(0);
             if (wait(vfull, 0)) dprob(0);
             for (int it = 0; it < total && ok && !__any_sync(0xffffffffu, *abort_flag); ++it) {
                 const int st = it % NST;
-                if (!wait(pready, it & 1)) break;
-                accumulate(tmem + TM_DV, tmem + TM_S, dom + st * (TILE >> 4), it > 0);
+                const bool more = it + 1 < total;
+                if (kOwn && more && wait(sfree, it & 1)) score(it + 1);
+                if (!ok || !wait(pready, it & 1)) break;
+                accumulate(tmem + TM_DV, tmem + TM_P, S::DO + st * TILE, it > 0);
                 tc_commit_warp(doempty + 8 * st);
-                if (it + 1 < total) score(it + 1);
-                if (!wait(dsready, it & 1)) break;
-                accumulate(tmem + TM_DK, tmem + TM_DP, qm + st * (TILE >> 4), it > 0);
+                if (!kOwn && more) score(it + 1);
+                if (kOwn && more && wait(dpfree, it & 1)) dprob(it + 1);
+                if (!ok || !wait(dsready, it & 1)) break;
+                accumulate(tmem + TM_DK, tmem + TM_DS, S::Q + st * TILE, it > 0);
                 tc_commit_warp(qempty + 8 * st);
-                if (it + 1 < total) dprob(it + 1);
+                if (!kOwn && more) dprob(it + 1);
             }
             tc_commit_warp(done);
             if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
@@ -392,8 +402,8 @@ struct AttnDqSmem {
     static constexpr int TILE = AT * D * 2;
     static constexpr int NST = D == 128 ? 5 : 8;
     static constexpr int RING = 2 * TILE;           // Q, dO, then K_0, V_0, K_1, V_1, ...
-    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready done
-    static constexpr int TMEM_SLOT = BAR + (2 * NST + 7) * 8;
+    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready done dpfree
+    static constexpr int TMEM_SLOT = BAR + (2 * NST + 8) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -427,12 +437,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int nt = seen_tile <= 0 ? 0 : (seen_tile + AT - 1) / AT;
 
     const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull = empty0 + 8 * NST, dofull = qfull + 8,
-                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready = qfull + 40, done = qfull + 48;
+                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready = qfull + 40, done = qfull + 48, dpfree = qfull + 56;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
         for (int s = 0; s < 2 * NST; ++s) mbar_init(full0 + 8 * s, 1);
         for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull, done}) mbar_init(b, 1);
         mbar_init(dsready, 8);
+        mbar_init(dpfree, 8);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -488,6 +499,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             tc_ld32(td, x[0]);
             tc_ld32(td + 32, x[1]);
             tc_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dpfree);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t w[16];
@@ -544,9 +558,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             }
         } else if (warp == 8 && nt > 0) {
             // ---------------- MMAs ----------------
-            const uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
-            const uint64_t qd = tile_desc_k(sb), dod = tile_desc_k(sb + TILE);
-            const uint64_t rk = tile_desc_k(sb + S::RING), rm = tile_desc_mn(sb + S::RING);
+            constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
+            const TileDesc desc(sb);
             const int tail = sq.lk - (nt - 1) * AT;  // rows of the last key tile, if fewer than 128
             bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -554,43 +567,34 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            // the tile at a ring position, with what follows the sequence taken out
-            auto arrived = [&](int pos) {
-                if (!wait(full0 + 8 * (pos % NST), (pos / NST) & 1)) return false;
-                if (tail < AT && (pos >> 1) == nt - 1) zero_tail_rows<D>(sb + S::RING + (pos % NST) * TILE, tail, lane);
-                return true;
-            };
-            auto product = [&](uint32_t d, uint64_t a, int pos) {
-                const uint64_t b = rk + (pos % NST) * (TILE >> 4);
+            auto place = [](int pos) { return S::RING + (pos % NST) * TILE; };  // ring positions: K_j at 2 j, V_j at 2 j + 1
+            // D[128 queries][128 keys] = (Q or dO) (K or V)^T, once the tile is there and what follows the sequence taken out
+            auto product = [&](uint32_t d, int rows, int pos, uint32_t commit) {
+                if (!wait(full0 + 8 * (pos % NST), (pos / NST) & 1)) return;
+                if (tail < AT && (pos >> 1) == nt - 1) zero_tail_rows<D>(sb + place(pos), tail, lane);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss_warp(d, a + kstep_k(ks), b + kstep_k(ks), id_s, ks > 0);
+                    tc_mma_ss_warp(d, desc.k(rows, ks), desc.k(place(pos), ks), id_s, ks > 0);
+                tc_commit_warp(commit);
             };
-            auto score = [&](int j) {  // S = Q K^T
-                if (!arrived(2 * j)) return;
-                product(tmem + TM_S + 128 * (j & 1), qd, 2 * j);
-                tc_commit_warp(sfull0 + 8 * (j & 1));
-            };
-            auto dprob = [&](int j) {  // dP = dO V^T
-                if (!arrived(2 * j + 1)) return;
-                product(tmem + TM_DP, dod, 2 * j + 1);
-                tc_commit_warp(dpfull);
-                tc_commit_warp(empty0 + 8 * ((2 * j + 1) % NST));
+            auto score = [&](int j) { product(tmem + TM_S + 128 * (j & 1), 0, 2 * j, sfull0 + 8 * (j & 1)); };
+            auto dprob = [&](int j) {
+                product(tmem + TM_DP, TILE, 2 * j + 1, dpfull);
+                if (ok) tc_commit_warp(empty0 + 8 * ((2 * j + 1) % NST));
             };
             if (wait(qfull, 0)) score(0);
             if (wait(dofull, 0)) dprob(0);
             if (ok && nt > 1) score(1);
             for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
-                if (!wait(dsready, j & 1)) break;
-                const uint64_t b = rm + ((2 * j) % NST) * (TILE >> 4);
                 const uint32_t a = tmem + TM_S + 128 * (j & 1);
-                if (j + 1 < nt) dprob(j + 1);
+                if (j + 1 < nt && wait(dpfree, j & 1)) dprob(j + 1);
+                if (!ok || !wait(dsready, j & 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
-                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 2) * 64 + (ks & 3) * 8, b + kstep_mn(ks), id_d,
+                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 2) * 64 + (ks & 3) * 8, desc.mn(place(2 * j), ks), id_d,
                                    j > 0 || ks > 0);
                 tc_commit_warp(empty0 + 8 * ((2 * j) % NST));
-                if (ok && j + 2 < nt) score(j + 2);
+                if (j + 2 < nt) score(j + 2);
             }
             tc_commit_warp(done);
             if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);

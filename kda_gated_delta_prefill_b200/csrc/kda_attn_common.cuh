@@ -62,6 +62,28 @@ __device__ __forceinline__ uint32_t kstep_k(int ks)
 }
 __device__ __forceinline__ uint32_t kstep_mn(int ks) { return static_cast<uint32_t>(ks * (2048 >> 4)); }
 
+// Descriptors of the tiles at byte offsets of the CTA's shared memory: a constant high word, and a low word (addresses
+// below 2^18 bytes) that only offsets are added to, so that an MMA costs its issuer little more than itself.
+struct TileDesc {
+    uint32_t khi, klo, mhi, mlo;
+    __device__ __forceinline__ explicit TileDesc(uint32_t sb)
+    {
+        const uint64_t k = tile_desc_k(sb), m = tile_desc_mn(sb);
+        khi = static_cast<uint32_t>(k >> 32);
+        klo = static_cast<uint32_t>(k);
+        mhi = static_cast<uint32_t>(m >> 32);
+        mlo = static_cast<uint32_t>(m);
+    }
+    __device__ __forceinline__ uint64_t k(int at, int ks) const  // step ks of 16 columns, rows are M or N
+    {
+        return (static_cast<uint64_t>(khi) << 32) | (klo + (at >> 4) + kstep_k(ks));
+    }
+    __device__ __forceinline__ uint64_t mn(int at, int ks) const  // step ks of 16 rows, columns are N
+    {
+        return (static_cast<uint64_t>(mhi) << 32) | (mlo + (at >> 4) + kstep_mn(ks));
+    }
+};
+
 // Rows [first, 128) of a tile become zero (whole warp; the async proxy sees it).  Tail tiles of a sequence hold
 // whatever follows it, and 0 * NaN in a matrix product would carry that into the sequence's results.
 template <int D>

@@ -271,11 +271,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             auto issue = [&](auto first, auto last) {
                 constexpr int w0 = decltype(first)::value, w1 = decltype(last)::value;
                 constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_o = idesc_bf16(128, D, false, true);
-                // descriptors: a constant high word, and a low word that only offsets below 2^18 bytes are added to
-                const uint64_t dk = tile_desc_k(sb), dm = tile_desc_mn(sb);
-                const uint32_t khi = static_cast<uint32_t>(dk >> 32), klo = static_cast<uint32_t>(dk);
-                const uint32_t mhi = static_cast<uint32_t>(dm >> 32), mlo = static_cast<uint32_t>(dm);
-                auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+                const TileDesc desc(sb);
                 bool ok = true;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     ok = ok && __all_sync(0xffffffffu, mbar_wait_quiet(bar, parity));
@@ -287,11 +283,10 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                 auto release = [&](int pos) { tc_commit_warp(empty0 + 8 * (pos % NST)); };
                 auto score = [&](int w, int j) {  // S_w = Q_w K_j^T
                     if (!arrived(2 * j)) return;
-                    const uint32_t b = klo + ((S::RING + ((2 * j) % NST) * TILE) >> 4);
+                    const int at = S::RING + ((2 * j) % NST) * TILE;
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma_ss_warp(tmem + 128 * w, desc(khi, klo + ((w * TILE) >> 4) + kstep_k(ks)),
-                                       desc(khi, b + kstep_k(ks)), id_s, ks > 0);
+                        tc_mma_ss_warp(tmem + 128 * w, desc.k(w * TILE, ks), desc.k(at, ks), id_s, ks > 0);
                     tc_commit_warp(sfull0 + 8 * w);
                 };
 #pragma unroll
@@ -306,14 +301,14 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                         if (kOwnP && j + 1 < nt[w] && wait(sfree0 + 8 * w, j & 1)) score(w, j + 1);
                         if (!ok || !arrived(2 * j + 1)) continue;
                         if (sq.lk - j * AT < AT) zero_tail_rows<D>(sb + S::RING + st * TILE, sq.lk - j * AT, lane);
-                        const uint32_t b = mlo + ((S::RING + st * TILE) >> 4);
+                        const int at = S::RING + st * TILE;
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             if (!wait(pready0 + 8 * (2 * w + hf), j & 1)) break;
 #pragma unroll
                             for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
                                 tc_mma_ts_warp(tmem + TM_O + D * w, tmem + TM_P + TM_PSTEP * w + 8 * ks,
-                                               desc(mhi, b + kstep_mn(ks)), id_o, j > 0 || ks > 0);
+                                               desc.mn(at, ks), id_o, j > 0 || ks > 0);
                         }
                         if (!ok) continue;
                         if (kOwnP || j + 1 == nt[w]) tc_commit_warp(odone0 + 8 * w);
