@@ -94,9 +94,13 @@ struct AttnDkvSmem {
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
-// 8 warps of arithmetic, one of MMAs, one of loads, two idle: three warpgroups for the register split
-// (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int kAttnBwdThreads = 384;
+// 16 warps of arithmetic (a quarter of the rows, 32 columns each), then one of MMAs, one of loads and two idle: five
+// warpgroups for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler and both
+// in the same step, most cycles issued nothing: TODO.
+constexpr int kAttnBwdWarps = 16, kAttnBwdThreads = 32 * (kAttnBwdWarps + 4);
+constexpr int kAttnBwdMma = kAttnBwdWarps, kAttnBwdLoad = kAttnBwdWarps + 1;
+#define ATTN_BWD_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n")
+#define ATTN_BWD_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n")
 
 template <int D>
 __global__ void __launch_bounds__(kAttnBwdThreads, 1)
@@ -106,9 +110,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 {
     using S = AttnDkvSmem<D>;
     constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
-    constexpr bool kOwn = D == 64;  // P and dS have columns of their own, in halves like those of S and dP
+    constexpr bool kOwn = D == 64;  // P and dS have columns of their own
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
-    constexpr uint32_t TM_P = kOwn ? 384 : TM_S, TM_DS = kOwn ? 448 : TM_DP, TM_HALF = kOwn ? 32 : 64;
+    constexpr uint32_t TM_P = kOwn ? 384 : TM_S, TM_DS = kOwn ? 448 : TM_DP, TM_GROUP = kOwn ? 16 : 32;  // 32 queries
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -130,11 +134,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < 4 * NST; ++s) mbar_init(qfull + 8 * s, 1);
         for (uint32_t b : {kfull, vfull, sfull, dpfull, done}) mbar_init(b, 1);
-        for (uint32_t b : {pready, dsready, sfree, dpfree}) mbar_init(b, 8);
+        for (uint32_t b : {pready, dsready, sfree, dpfree}) mbar_init(b, kAttnBwdWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
+    if (warp == kAttnBwdMma) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -144,13 +148,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         *abort_flag = 1;
     };
 
-    if (warp < 8) {
-        // ---------------- P^T and dS^T: key row, half of the query columns ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        const int half = warp >> 2, quarter = warp & 3;
+    if (warp < kAttnBwdWarps) {
+        // ---------------- P^T and dS^T: key row, 32 of the query columns ----------------
+        ATTN_BWD_MORE_REGISTERS();
+        const int group = warp >> 2, quarter = warp & 3;
         const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t ts = tmem + lb + TM_S + 64 * half, td = tmem + lb + TM_DP + 64 * half;
-        const uint32_t tp = tmem + lb + TM_P + TM_HALF * half, tds = tmem + lb + TM_DS + TM_HALF * half;
+        const uint32_t ts = tmem + lb + TM_S + 32 * group, td = tmem + lb + TM_DP + 32 * group;
+        const uint32_t tp = tmem + lb + TM_P + TM_GROUP * group, tds = tmem + lb + TM_DS + TM_GROUP * group;
         auto arrive = [&](uint32_t bar) {
             tc_fence_before();
             __syncwarp();
@@ -170,21 +174,20 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            uint32_t r[2][32];
-            tc_ld32(ts, r[0]);
-            tc_ld32(ts + 32, r[1]);
-            const float4 *l2 = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 16 * half;
+            uint32_t r[32];
+            tc_ld32(ts, r);
+            const float4 *l2 = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 8 * group;
             const float4 *dl = l2 + 32;
             tc_wait_ld();
             if (kOwn) arrive(sfree);
             // queries q >= key - diff see the key
-            const int from = key - diff - i * AT - 64 * half;
+            const int from = key - diff - i * AT - 32 * group;
             const bool cut = __any_sync(0xffffffffu, from > 0);
-            float2 pr[32];
+            float2 pr[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
                 const float4 l = l2[e];
-                uint32_t *x = &r[e >> 3][4 * (e & 7)];
+                const uint32_t *x = &r[4 * e];
                 float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c, c),
                                 make_float2(-l.x, -l.y));
                 float2 b = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c, c),
@@ -202,43 +205,33 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             }
             ok = reusable(doempty, it);
             if (!ok) break;
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(pr[16 * k + e].x, pr[16 * k + e].y);
-                tc_st16(tp + 16 * k, w);
-            }
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16(pr[e].x, pr[e].y);
+            tc_st16(tp, w);
             tc_wait_st();
             arrive(pready);
 
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, it & 1));
             if (!ok) break;
             tc_fence_after();
-            tc_ld32(td, r[0]);
-            tc_ld32(td + 32, r[1]);
+            tc_ld32(td, r);
             tc_wait_ld();
             if (kOwn) arrive(dpfree);
             ok = reusable(qempty, it);
             if (!ok) break;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 d4 = dl[8 * k + e];
-                    const uint32_t *x = &r[k][4 * e];
-                    const float2 a = mul2(pr[16 * k + 2 * e],
-                                          add2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                               make_float2(-d4.x, -d4.y)));
-                    const float2 b = mul2(pr[16 * k + 2 * e + 1],
-                                          add2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                               make_float2(-d4.z, -d4.w)));
-                    w[2 * e] = pack_bf16(a.x, a.y);
-                    w[2 * e + 1] = pack_bf16(b.x, b.y);
-                }
-                tc_st16(tds + 16 * k, w);
+            for (int e = 0; e < 8; ++e) {
+                const float4 d4 = dl[e];
+                const uint32_t *x = &r[4 * e];
+                const float2 a = mul2(pr[2 * e], add2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                                      make_float2(-d4.x, -d4.y)));
+                const float2 b = mul2(pr[2 * e + 1], add2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                                          make_float2(-d4.z, -d4.w)));
+                w[2 * e] = pack_bf16(a.x, a.y);
+                w[2 * e + 1] = pack_bf16(b.x, b.y);
             }
+            tc_st16(tds, w);
             tc_wait_st();
             arrive(dsready);
         }
@@ -246,24 +239,27 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else if (p.split > 1 && total > 0) {
-            // this CTA's sums over its heads, fp32, to shared memory: dV, then dK (nothing else uses the tiles any more)
+            // this CTA's sums over its heads, fp32, to shared memory: dV (groups 0, 1: half the columns each), dK (2, 3); nothing
+            // else uses the tiles any more
             tc_fence_after();
+            const int half = group >> 1, c0 = (group & 1) * (D / 2);
             const int row = 32 * quarter + lane;
             float4 *dst = reinterpret_cast<float4 *>(sm) + (half * AT + row) * (D / 4);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < D / 64; ++i) {
                 uint32_t v[32];
-                tc_ld32(tmem + lb + (half ? TM_DK : TM_DV) + 32 * i, v);
+                tc_ld32(tmem + lb + (half ? TM_DK : TM_DV) + c0 + 32 * i, v);
                 tc_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    dst[(8 * i + e) ^ (row & (D / 4 - 1))] =
+                    dst[(c0 / 4 + 8 * i + e) ^ (row & (D / 4 - 1))] =
                         make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                     __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
             }
-        } else if (rank == 0) {
+        } else if (rank == 0 && group < 2) {
             // warps 0-3 store dV, 4-7 dK, through the K and V tiles (no MMA reads them any more)
             tc_fence_after();
+            const int half = group;
             const int row = j0 + 32 * quarter;
             const int64_t at = ((static_cast<int64_t>(sq.k0) + row) * p.HKV + hk) * D;
             store_rows<D>(tmem + lb + (half ? TM_DK : TM_DV), total > 0, half ? p.scale : 1.f,
@@ -271,13 +267,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                           static_cast<int64_t>(p.HKV) * D);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (warp == 10 && lane == 0) {
+        ATTN_BWD_FEWER_REGISTERS();
+        if (warp == kAttnBwdLoad + 1 && lane == 0) {
             // (also in CTAs without work.)  The statistics are complete behind the wait, so dQ may start, where SMs are idle
             asm volatile("griddepcontrol.wait;\n" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
         }
-        if (warp == 9 && lane == 0 && total > 0) {
+        if (warp == kAttnBwdLoad && lane == 0 && total > 0) {
             // ---------------- loads ----------------
             asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the statistics (nothing else depends on that launch)
             int nqi = 0, ndo = 0;  // tiles of Q and of dO requested
@@ -318,7 +314,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 for (int i = max(0, nqi - NST); i < nqi; ++i) mbar_wait(qfull + 8 * (i % NST), (i / NST) & 1);
                 for (int i = max(0, ndo - NST); i < ndo; ++i) mbar_wait(dofull + 8 * (i % NST), (i / NST) & 1);
             }
-        } else if (warp == 8 && total > 0) {
+        } else if (warp == kAttnBwdMma && total > 0) {
             // ---------------- MMAs ----------------
             constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
             const TileDesc desc(sb);
@@ -341,11 +337,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             };
             auto score = [&](int it) { product(tmem + TM_S, 0, S::Q, qfull, sfull, it); };
             auto dprob = [&](int it) { product(tmem + TM_DP, TILE, S::DO, dofull, dpfull, it); };
-            // D += A B, A in two halves of 64 queries
+            // D += A B, A in groups of 32 queries
             auto accumulate = [&](uint32_t d, uint32_t a, int at, bool more) {
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
-                    tc_mma_ts_warp(d, a + (ks >> 2) * TM_HALF + (ks & 3) * 8, desc.mn(at, ks), id_d, more || ks > 0);
+                    tc_mma_ts_warp(d, a + (ks >> 1) * TM_GROUP + (ks & 1) * 8, desc.mn(at, ks), id_d, more || ks > 0);
             };
             if (wait(kfull, 0)) score(0);
             if (wait(vfull, 0)) dprob(0);
@@ -369,13 +365,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc_dealloc(tmem, TM_COLS);
+    if (warp == kAttnBwdMma) tc_dealloc(tmem, TM_COLS);
     if (p.split > 1 && total > 0) {
         // the cluster's sums: each CTA adds up its share of the rows over all CTAs, in their order
         cluster_sync();
         constexpr int Q4 = D / 4;
         const int rows = AT / p.split, r0 = rank * rows;
-        for (int i = tid; warp < 8 && i < 2 * rows * Q4; i += 256) {  // (the other warps gave their registers away)
+        for (int i = tid; warp < kAttnBwdWarps && i < 2 * rows * Q4; i += 32 * kAttnBwdWarps) {  // (the other warps gave their registers away)
             const int half = i / (rows * Q4), row = r0 + i / Q4 % rows, ch = i % Q4;
             const uint32_t at = sb + ((half * AT + row) * Q4 + (ch ^ (row & (Q4 - 1)))) * 16;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -442,12 +438,12 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < 2 * NST; ++s) mbar_init(full0 + 8 * s, 1);
         for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull, done}) mbar_init(b, 1);
-        mbar_init(dsready, 8);
-        mbar_init(dpfree, 8);
+        mbar_init(dsready, kAttnBwdWarps);
+        mbar_init(dpfree, kAttnBwdWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
+    if (warp == kAttnBwdMma) tc_alloc(sb + S::TMEM_SLOT, TM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -457,35 +453,33 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         *abort_flag = 1;
     };
 
-    if (warp < 8) {
-        // ---------------- P and dS: query row, half of the key columns ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        const int half = warp >> 2, quarter = warp & 3;
+    if (warp < kAttnBwdWarps) {
+        // ---------------- P and dS: query row, 32 of the key columns ----------------
+        ATTN_BWD_MORE_REGISTERS();
+        const int group = warp >> 2, quarter = warp & 3;
         const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t td = tmem + lb + TM_DP + 64 * half;
+        const uint32_t td = tmem + lb + TM_DP + 32 * group;
         const int r = 32 * quarter + lane;
         const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
         const float l2 = stat[r], delta = stat[AT + r];
-        const int seen = r0 + r + 1 + diff - 64 * half;  // keys of this half that the row sees (rows past the end: p = 0)
+        const int seen = r0 + r + 1 + diff - 32 * group;  // keys of this group that the row sees (rows past the end: p = 0)
         const float c = p.scale_log2;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            const uint32_t ts = tmem + lb + TM_S + 128 * (j & 1) + 64 * half;
+            const uint32_t ts = tmem + lb + TM_S + 128 * (j & 1) + 32 * group;
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(sfull0 + 8 * (j & 1), (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[2][32];
-            tc_ld32(ts, x[0]);
-            tc_ld32(ts + 32, x[1]);
+            uint32_t x[32];
+            tc_ld32(ts, x);
             tc_wait_ld();
             const int keys = seen - j * AT;
-            const bool cut = __any_sync(0xffffffffu, keys < 64);
-            float2 pr[32];
+            const bool cut = __any_sync(0xffffffffu, keys < 32);
+            float2 pr[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const uint32_t *y = &x[e >> 4][2 * (e & 15)];
-                float2 a = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), make_float2(c, c),
-                                make_float2(-l2, -l2));
+            for (int e = 0; e < 16; ++e) {
+                float2 a = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                make_float2(c, c), make_float2(-l2, -l2));
                 a = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
                 if (cut) {
                     if (2 * e >= keys) a.x = 0.f;
@@ -496,24 +490,19 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, j & 1));
             if (!ok) break;
             tc_fence_after();
-            tc_ld32(td, x[0]);
-            tc_ld32(td + 32, x[1]);
+            tc_ld32(td, x);
             tc_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dpfree);
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 a = mul2(pr[16 * k + e], add2(make_float2(__uint_as_float(x[k][2 * e]),
-                                                                           __uint_as_float(x[k][2 * e + 1])),
-                                                               make_float2(-delta, -delta)));
-                    w[e] = pack_bf16(a.x, a.y);
-                }
-                tc_st16(ts + 16 * k, w);
+            for (int e = 0; e < 16; ++e) {
+                const float2 a = mul2(pr[e], add2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                                  make_float2(-delta, -delta)));
+                w[e] = pack_bf16(a.x, a.y);
             }
+            tc_st16(ts, w);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -522,7 +511,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
-        } else if (half == 0) {
+        } else if (group == 0) {
             // through the Q tile (no MMA reads it any more)
             tc_fence_after();
             const int row = r0 + 32 * quarter;
@@ -530,8 +519,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                           p.dq + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D, static_cast<int64_t>(p.H) * D);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (warp == 9 && lane == 0 && nt > 0) {
+        ATTN_BWD_FEWER_REGISTERS();
+        if (warp == kAttnBwdLoad && lane == 0 && nt > 0) {
             // ---------------- loads ----------------
             const int hk = h / (p.H / p.HKV);
             bool ok = true;
@@ -556,7 +545,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 if (issued) mbar_wait(dofull, 0);
                 for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
             }
-        } else if (warp == 8 && nt > 0) {
+        } else if (warp == kAttnBwdMma && nt > 0) {
             // ---------------- MMAs ----------------
             constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
             const TileDesc desc(sb);
@@ -591,7 +580,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 if (!ok || !wait(dsready, j & 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
-                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 2) * 64 + (ks & 3) * 8, desc.mn(place(2 * j), ks), id_d,
+                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 1) * 32 + (ks & 1) * 8, desc.mn(place(2 * j), ks), id_d,
                                    j > 0 || ks > 0);
                 tc_commit_warp(empty0 + 8 * ((2 * j) % NST));
                 if (j + 2 < nt) score(j + 2);
@@ -602,7 +591,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc_dealloc(tmem, TM_COLS);
+    if (warp == kAttnBwdMma) tc_dealloc(tmem, TM_COLS);
     linger();
 }
 
