@@ -504,26 +504,41 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
         return KDA_ERR_CUDA;
     const int grid = static_cast<int>(std::min<int64_t>(ctas, static_cast<int64_t>(info.sms) * ad_ctas(hb / 8)));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // few short requests: a cluster per unit
+    const int64_t units = static_cast<int64_t>(B) * HKV * p.chunks;
+    const bool clusters = units * kAdCluster <= static_cast<int64_t>(info.sms) * ad_ctas(hb / 8) &&
+                          static_cast<int64_t>(table_width) * block_size <= kAdClusterTiles * ad_tile(D);
+    auto launch = [&](auto kern, int blocks, int threads, int smem, cudaLaunchAttribute attr, auto... args) {
+        if (smem && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(blocks);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = &attr;
+        cfg.numAttrs = attr.id == cudaLaunchAttributeIgnore ? 0 : 1;
+        return cudaLaunchKernelEx(&cfg, kern, p, args...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    };
     auto go = [&](auto fp8, auto d, auto nt) {
         constexpr bool F = decltype(fp8)::value;
         constexpr int DD = decltype(d)::value, N = decltype(nt)::value;
-        auto kern = kda_attn_decode_kernel<F, DD, N>;
         constexpr int smem = AttnDecodeSmem<DD, N>::TOTAL;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return KDA_ERR_CUDA;
-        kern<<<grid, kAdThreads, smem, s>>>(p, mk, mv, shift);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-        // the join waits for the pieces on the device (griddepcontrol.wait), so its launch overlaps the step
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(kAdJoinThreads);
-        cfg.stream = s;
         cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeIgnore;
+        if (clusters) {
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = kAdCluster;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            return launch(kda_attn_decode_kernel<F, DD, N, true>, static_cast<int>(units * kAdCluster), kAdThreads, smem, attr,
+                          mk, mv, shift);
+        }
+        kda_status_t r = launch(kda_attn_decode_kernel<F, DD, N, false>, grid, kAdThreads, smem, attr, mk, mv, shift);
+        if (r != KDA_OK) return r;
+        // the join waits for the pieces on the device (griddepcontrol.wait), so its launch overlaps the step
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kda_attn_decode_join_kernel<DD, N>, p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        return launch(kda_attn_decode_join_kernel<DD, N>, grid, kAdJoinThreads, 0, attr);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

@@ -100,7 +100,7 @@ __device__ __forceinline__ void zero_tail_rows(uint32_t tile, int first, int lan
     __syncwarp();
 }
 
-// Thread-block clusters: a barrier of all their threads, and four floats of CTA `rank`'s shared memory.
+// Thread-block clusters: a barrier of all their threads, and four or two floats of CTA `rank`'s shared memory.
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -112,6 +112,17 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t saddr, int rank)
         "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
         " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(saddr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 cluster_load2(uint32_t saddr, int rank)
+{
+    float2 v;
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %2, %3;\n ld.shared::cluster.v2.f32 {%0, %1}, [a];\n}\n"
+        : "=f"(v.x), "=f"(v.y)
         : "r"(saddr), "r"(rank)
         : "memory");
     return v;
