@@ -10,7 +10,7 @@
 // launch joins them in the order of the CTAs.
 //
 // Few short requests take another form: a cluster of eight CTAs per unit, which join over distributed shared memory, with
-// no scan of the lengths and no second launch (one request of 777 tokens, 32/8 heads: 5.8 us on the device, 9.2 in the other).
+// no scan of the lengths and no second launch (one request of 777 tokens, 32/8 heads: 5.8 us on the device, 8.9 in the other).
 //
 // In a CTA, one warp requests the tiles' pages by TMA through a ring; four warps take 16 tokens of a tile each, with a
 // running softmax of their own, and join at the end of the unit.  All query heads of a group share one pass over the
@@ -35,8 +35,9 @@ namespace kda {
 __host__ __device__ constexpr int ad_tile(int D) { return 64 * (128 / D); }
 __host__ __device__ constexpr int ad_ctas(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
-// The form for few short requests: CTAs of a unit, and the most tiles that its table may hold.
-constexpr int kAdCluster = 8, kAdClusterTiles = 64;
+// The form for few short requests: CTAs of a unit, and the most tiles that its table may hold (one request, 32/8 heads,
+// D = 128; us on the device with a cluster and without: 500 tokens 5.4, 8.5; 2,000: 7.1, 10.2; 8,000: 13, 15; 32,000: 37, 21).
+constexpr int kAdCluster = 8, kAdClusterTiles = 128;
 
 struct AttnDecodeParams {
     const __nv_bfloat16 *q;  // row b at q + b * q_stride: [H, D]
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
         const int per = (p.B + kAdThreads - 1) / kAdThreads;
         const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        for (int i = b0; i < b1; ++i) mine += tiles_of(i);
         int64_t inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -186,19 +187,19 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
         const int64_t g0 = c < G ? share(W, c, G) : 0;
         g1 = c < G ? share(W, c + 1, G) : 0;
         // rows without tokens: zeros (every CTA some of them); too long for the table: an error
-        for (int b = c; b < p.B; b += gridDim.x) {
-            if (p.lens[b] > cap && tid == 0) atomicOr(p.err, ERR_BLOCK_ID);
-            if (len_of(b) > 0) continue;
+        for (int row = c; row < p.B; row += gridDim.x) {
+            if (p.lens[row] > cap && tid == 0) atomicOr(p.err, ERR_BLOCK_ID);
+            if (len_of(row) > 0) continue;
             for (int i = tid; i < p.H * D / 2; i += kAdThreads)
-                reinterpret_cast<uint32_t *>(p.o + static_cast<int64_t>(b) * p.H * D)[i] = 0u;
-            for (int i = tid; i < p.H; i += kAdThreads) p.lse[static_cast<int64_t>(b) * p.H + i] = -INFINITY;
+                reinterpret_cast<uint32_t *>(p.o + static_cast<int64_t>(row) * p.H * D)[i] = 0u;
+            for (int i = tid; i < p.H; i += kAdThreads) p.lse[static_cast<int64_t>(row) * p.H + i] = -INFINITY;
         }
         int *start = reinterpret_cast<int *>(sm + S::SCAN + 64);
         if (g0 < g1 && g0 >= before * units_row && g0 < (before + mine) * units_row) {
             int64_t at = before;
-            int b = b0;
-            for (; g0 >= (at + tiles_of(b)) * units_row; ++b) at += tiles_of(b);
-            start[0] = b;
+            int row = b0;
+            for (; g0 >= (at + tiles_of(row)) * units_row; ++row) at += tiles_of(row);
+            start[0] = row;
             *reinterpret_cast<int64_t *>(start + 2) = g0 - at * units_row;
         }
         if (tid == 0) p.shared_unit[c] = make_int2(-1, 0);
@@ -606,56 +607,73 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
     }
 }
 
-// Joins the pieces of a unit that began in CTA c, in their order: a thread per head and four dims.  Bound by the latency of
-// three dependent loads (which unit, the pieces' references, their accumulators).
-constexpr int kAdJoinThreads = 256;
+// Joins the pieces of a unit that began in CTA c, in their order.  A thread takes a head, four dims and a run of the
+// pieces; the runs are joined through shared memory.  Bound by the latency of its dependent loads (which unit; references
+// and accumulators, eight pieces at a time).
+constexpr int kAdJoinThreads = 512;
+struct AttnPiece {
+    float M, l;
+    float4 a;
+    __device__ __forceinline__ void add(float Mk, float lk, float4 v)  // the other's reference at most M
+    {
+        const float f = Mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : ex2(Mk - M);
+        l = fmaf(lk, f, l);
+        a = make_float4(fmaf(v.x, f, a.x), fmaf(v.y, f, a.y), fmaf(v.z, f, a.z), fmaf(v.w, f, a.w));
+    }
+    __device__ __forceinline__ void refer(float Mn)
+    {
+        const float f = M == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(M - Mn);
+        M = Mn;
+        l *= f;
+        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    }
+};
 template <int D, int NT>
 __global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(const AttnDecodeParams p)
 {
     constexpr int HB = 8 * NT, PIECE = HB * (D + 2);
+    __shared__ AttnPiece runs[kAdJoinThreads];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, tid = threadIdx.x;
     const int2 su = p.shared_unit[c];
     if (su.x < 0) return;
     const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
     const int b = su.x / units_row, u = su.x % units_row, hk = u / p.chunks, hc = u % p.chunks;
-    const int heads = min(HB, group - hc * HB);
+    const int heads = min(HB, group - hc * HB), items = heads * (D / 4), nr = kAdJoinThreads / items;  // runs
+    const int item = tid % items, run = tid / items, hd = item / (D / 4), d = 4 * (item % (D / 4));
+    const int n = su.y + 1, k_begin = n * run / nr, k_end = run < nr ? n * (run + 1) / nr : 0;
     // the piece of CTA c is its last one, those of the CTAs behind their first
     const float *first = p.part + (2ll * c + 1) * PIECE, *rest = p.part + 2ll * c * PIECE;
-    auto piece = [&](int k) { return k == 0 ? first : rest + 2ll * k * PIECE; };
-    for (int i = threadIdx.x; i < heads * (D / 4); i += kAdJoinThreads) {
-        const int hd = i / (D / 4), d = 4 * (i % (D / 4));
-        float M = -INFINITY, l = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 <= su.y; k0 += 8) {  // eight pieces' loads in flight
-            float2 ml[8];
-            float4 v[8];
+    AttnPiece all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = k_begin; k0 < k_end; k0 += 8) {
+        float2 ml[8];
+        float4 v[8];
+        float M = all.M;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k <= su.y) {
-                    const float *src = piece(k0 + k);
-                    ml[k] = *reinterpret_cast<const float2 *>(src + HB * D + 2 * hd);
-                    v[k] = *reinterpret_cast<const float4 *>(src + hd * D + d);
-                }
+        for (int k = 0; k < 8; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < k_end) {
+                const float *src = k0 + k == 0 ? first : rest + 2ll * (k0 + k) * PIECE;
+                ml[k] = *reinterpret_cast<const float2 *>(src + HB * D + 2 * hd);
+                v[k] = *reinterpret_cast<const float4 *>(src + hd * D + d);
             }
-            float Mn = M;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) Mn = fmaxf(Mn, ml[k].x);
-            const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
-            l *= f0;
-            a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - Mn);
-                l = fmaf(ml[k].y, f, l);
-                a = make_float4(fmaf(v[k].x, f, a.x), fmaf(v[k].y, f, a.y), fmaf(v[k].z, f, a.z), fmaf(v[k].w, f, a.w));
-            }
-            M = Mn;
         }
-        store_attention<D>(p, b, hk * group + hc * HB + hd, d, a, M, l);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) M = fmaxf(M, ml[k].x);
+        all.refer(M);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) all.add(ml[k].x, ml[k].y, v[k]);
     }
+    runs[tid] = all;
+    __syncthreads();
+    if (run > 0) return;
+    for (int r = 1; r < nr; ++r) {
+        const AttnPiece &o = runs[r * items + item];
+        all.refer(fmaxf(all.M, o.M));
+        all.add(o.M, o.l, o.a);
+    }
+    store_attention<D>(p, b, hk * group + hc * HB + hd, d, all.a, all.M, all.l);
 }
 
 }  // namespace kda
