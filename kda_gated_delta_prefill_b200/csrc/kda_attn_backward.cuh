@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x % p.split, unit = blockIdx.x / p.split;
-    const int hk = unit % p.HKV, slot = unit / p.HKV, G = p.H / p.HKV / p.split, head0 = (hk * p.split + rank) * G;
+    const int hk = unit % p.HKV, G = p.H / p.HKV / p.split, head0 = (hk * p.split + rank) * G;
     int n, blk;
-    if (!find_block<AT>(p.seq.cu_k, p.seq.N, p.seq.Tk, slot, lane, n, blk)) return;
+    if (!pick_block<AT, false>(p.seq.cu_k, p.seq.N, p.seq.Tk, unit / p.HKV, lane, n, blk)) return;
     const Seq sq = seq_of(p.seq, n);
     const int diff = sq.lk - sq.lq, j0 = blk * AT;
     // query tiles that see a key of this tile: first .. nq - 1 of each of this CTA's heads
@@ -416,14 +416,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % p.H, slot = p.qslots - 1 - blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H;
     int n, blk;
     // dQ may start while dK/dV runs and has no use for it, but what follows in the stream waits for this launch only: the last
     // CTA stays until dK/dV is complete
     auto linger = [] {
         if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     };
-    if (!find_block<AT>(p.seq.cu_q, p.seq.N, p.seq.T, slot, lane, n, blk)) {
+    if (!pick_block<AT, true>(p.seq.cu_q, p.seq.N, p.seq.T, blockIdx.x / p.H, lane, n, blk)) {
         linger();
         return;
     }
@@ -460,6 +460,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const uint32_t lb = static_cast<uint32_t>(32 * quarter) << 16;
         const uint32_t td = tmem + lb + TM_DP + 32 * group;
         const int r = 32 * quarter + lane;
+        const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + blk;
         const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
         const float l2 = stat[r], delta = stat[AT + r];
         const int seen = r0 + r + 1 + diff - 32 * group;  // keys of this group that the row sees (rows past the end: p = 0)

@@ -230,6 +230,59 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, 
     }
 }
 
+// The sequence and block of the t-th CTA (of block_slots<BLK>()), those with most work first: blocks in levels by their place
+// in their sequence, the last ones first (LAST) or the first ones.  With up to 128 packed sequences a warp holds
+// their block counts and searches for the level; with more, blocks go in the order of their slots.
+template <int BLK, bool LAST>
+__device__ __forceinline__ bool pick_block(const int32_t *cu, int N, int T, int t, int lane, int &n, int &blk)
+{
+    const uint32_t all = 0xffffffffu;
+    if (!cu) {
+        const int level = t / N;
+        n = t - level * N;
+        blk = LAST ? (T + BLK - 1) / BLK - 1 - level : level;
+        return true;
+    }
+    if (N > 128) return find_block<BLK>(cu, N, T, LAST ? block_slots<BLK>(N, T, true) - 1 - t : t, lane, n, blk);
+    int nb[4], most = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = lane + 32 * k;
+        int first, len = 0;
+        if (i < N) seq_range(cu, i, T, first, len);
+        nb[k] = (len + BLK - 1) / BLK;
+        most = max(most, nb[k]);
+    }
+    most = __reduce_max_sync(all, most);
+    // CTAs before level b: blocks at places above b, or below it
+    auto before = [&](int b) {
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c += LAST ? max(nb[k] - b - 1, 0) : min(nb[k], b);
+        return static_cast<int>(__reduce_add_sync(all, static_cast<unsigned>(c)));
+    };
+    if (t >= before(LAST ? -1 : most)) return false;
+    int lo = 0, hi = most;  // the level is in [lo, hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        // LAST: levels mid .. hi - 1 hold the CTAs before before(mid - 1)
+        if (LAST ? t < before(mid - 1) : t >= before(mid)) lo = mid;
+        else hi = mid;
+    }
+    blk = lo;
+    int r = t - before(lo);  // the r-th sequence that has this block
+    n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t m = __ballot_sync(all, nb[k] > lo);
+        const int c = __popc(m);
+        const uint32_t it = __ballot_sync(all, (m >> lane & 1) && __popc(m & ((1u << lane) - 1)) == r);
+        if (r >= 0 && r < c) n = 32 * k + __ffs(it) - 1;
+        r -= c;
+    }
+    return true;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 }  // namespace kda

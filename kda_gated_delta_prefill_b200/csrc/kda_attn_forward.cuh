@@ -72,9 +72,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // heads of one block of queries beside one another (they share keys), the blocks with most keys first
     const int h = blockIdx.x % p.H;
-    const int slot = p.slots - 1 - blockIdx.x / p.H;
     int n, blk;
-    if (!find_block<kAttnFwdRows>(p.seq.cu_q, p.seq.N, p.seq.T, slot, lane, n, blk)) return;
+    if (!pick_block<kAttnFwdRows, true>(p.seq.cu_q, p.seq.N, p.seq.T, blockIdx.x / p.H, lane, n, blk)) return;
     const Seq sq = seq_of(p.seq, n);
     const int diff = sq.lk - sq.lq, r0 = blk * kAttnFwdRows;
     // key tiles that tile w (0, 1) of the block sees
