@@ -126,6 +126,17 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         const float c = p.scale_log2;
         float m = 0.f, l = 0.f;  // reference (in units of the scores), sum
         bool ok = true;
+        auto rescale = [&](float alpha) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t ov[16];
+                tc_ld16(to + 16 * i, ov);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                tc_st16(to + 16 * i, ov);
+            }
+        };
         for (int j = 0; j < nt[w]; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(sfull0 + 8 * w, j & 1));
             if (!ok) break;
@@ -158,33 +169,22 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                 mx[i] = fmaxf(mx[i], __uint_as_float(r[i][31]));
             }
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            float alpha = 1.f;
             if (j == 0) {
                 m = top == -INFINITY ? 0.f : top;
-            } else {
-                // a row that has seen no key yet (l == 0) takes its first finite maximum as the reference
-                const bool grow = (top - m) * c > 8.f || (l == 0.f && top != -INFINITY);
-                if (kOwnP) {  // O += P V of the tile before has read P and written O
-                    ok = __all_sync(0xffffffffu, mbar_wait_quiet(odone0 + 8 * w, (j - 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float mn = grow ? top : m;
-                    const float alpha = l == 0.f ? 0.f : ex2((m - mn) * c);
-                    m = mn;
-                    l *= alpha;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t ov[32];
-                        tc_ld32(to + 32 * i, ov);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        tc_st32(to + 32 * i, ov);
-                    }
-                }
+            } else if ((top - m) * c > 8.f || (l == 0.f && top != -INFINITY)) {
+                // (a row that has seen no key yet takes its first finite maximum as the reference)
+                alpha = l == 0.f ? 0.f : ex2((m - top) * c);
+                m = top;
+                l *= alpha;
             }
-            // P in two halves of 64 keys: the MMAs start on the first while the second is formed
+            const bool move = __any_sync(0xffffffffu, alpha != 1.f);
+            if (kOwnP && j > 0) {  // O += P V of the tile before has read P and written O
+                ok = __all_sync(0xffffffffu, mbar_wait_quiet(odone0 + 8 * w, (j - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (move) rescale(alpha);
+            }
             const float2 c2 = make_float2(c, c), b2 = make_float2(-m * c, -m * c);
             float2 sum = make_float2(0.f, 0.f), sum1 = sum;
 #pragma unroll
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     else sum = add2(sum, x);
                     pk[e] = pack_bf16(x.x, x.y);
                 }
+                if (!kOwnP && i == 0 && move) rescale(alpha);  // (off the way to the first exponentials)
                 tc_st16(tp + 16 * i, pk);
                 if (i & 1) {
                     tc_wait_st();
