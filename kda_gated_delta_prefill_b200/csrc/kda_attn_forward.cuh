@@ -280,7 +280,11 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                 };
                 // ring positions: K_j at 2 j, V_j at 2 j + 1
                 auto arrived = [&](int pos) { return wait(full0 + 8 * (pos % NST), (pos / NST) & 1); };
-                auto release = [&](int pos) { tc_commit_warp(empty0 + 8 * (pos % NST)); };
+                // An issuer lets go of every position, also of those that its tile does not use, but of none before it is
+                // there: an arrival ahead of the loads would count for the position's predecessor in the ring.
+                auto release = [&](int pos) {
+                    if (arrived(pos)) tc_commit_warp(empty0 + 8 * (pos % NST));
+                };
                 auto score = [&](int w, int j) {  // S_w = Q_w K_j^T
                     if (!arrived(2 * j)) return;
                     const int at = S::RING + ((2 * j) % NST) * TILE;

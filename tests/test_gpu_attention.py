@@ -102,6 +102,11 @@ CASES = [
     (2, 300, 40, 4, 2, 128, None, None),      # rows that see nothing
     (1, 300, 44, 2, 2, 64, None, None),       # the whole first block sees nothing
     (1, 2500, 2500, 2, 1, 128, None, None),
+    (1, 2100, 2100, 3, 1, 64, None, None),    # the second half of the last block is empty, its first sees 17 key tiles
+    (1, 2350, 2350, 2, 2, 64, None, None),
+    (1, 4000, 4000, 2, 1, 64, [1700, 80, 1300, 130, 790], None),
+    (1, 100, 3000, 4, 2, 64, None, None),
+    (1, 100, 3000, 4, 2, 128, None, None),
     (1, 905, 905, 8, 2, 128, [1, 63, 64, 65, 0, 127, 128, 129, 328], None),
     (1, 1025, 1025, 4, 1, 64, [512, 1, 511, 0, 1], None),
     (1, 278, 707, 8, 2, 128, [200, 1, 0, 77], [456, 1, 200, 50]),
