@@ -11,6 +11,12 @@
 // order: no atomics, the same bits every time.  The price is that S and dP are formed twice (7 matrix products
 // instead of 5).
 //
+// Precision.  P and dS are rounded to bf16 for the products (2^-9 relative), and delta inherits the rounding of o: where one
+// key has most of a row's probability, dP_ij - delta_i is a small difference of it.  dQ and dK are 2.5e-3 off for scores of
+// unit variance and up to 5e-3 where the softmax is all but one-hot (of the 2-norm; 1.7e-3 is bf16 results alone).
+// delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then has to follow dQ, and a
+// backward took 15-40 % longer.
+//
 // dK/dV works on the transposes: a thread owns a key row of S^T = K Q^T and dP^T = V dO^T, so P^T and dS^T go back to
 // TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
 // TMEM (D = 128): S^T/P^T, dP^T/dS^T, dV, dK with 128 columns each.  The order of the MMAs,
@@ -398,8 +404,8 @@ struct AttnDqSmem {
     static constexpr int TILE = AT * D * 2;
     static constexpr int NST = D == 128 ? 5 : 8;
     static constexpr int RING = 2 * TILE;           // Q, dO, then K_0, V_0, K_1, V_1, ...
-    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready done dpfree
-    static constexpr int TMEM_SLOT = BAR + (2 * NST + 8) * 8;
+    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready[2] done dpfree
+    static constexpr int TMEM_SLOT = BAR + (2 * NST + 9) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -433,12 +439,12 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int nt = seen_tile <= 0 ? 0 : (seen_tile + AT - 1) / AT;
 
     const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull = empty0 + 8 * NST, dofull = qfull + 8,
-                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready = qfull + 40, done = qfull + 48, dpfree = qfull + 56;
+                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready0 = qfull + 40, done = qfull + 56, dpfree = qfull + 64;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
         for (int s = 0; s < 2 * NST; ++s) mbar_init(full0 + 8 * s, 1);
         for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull, done}) mbar_init(b, 1);
-        mbar_init(dsready, kAttnBwdWarps);
+        for (int b = 0; b < 2; ++b) mbar_init(dsready0 + 8 * b, kAttnBwdWarps);
         mbar_init(dpfree, kAttnBwdWarps);
         *abort_flag = 0;
         fence_mbar_init();
@@ -507,7 +513,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dsready);
+            if (lane == 0) mbar_arrive(dsready0 + 8 * (j & 1));
         }
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
         if (!ok) {
@@ -578,7 +584,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
                 const uint32_t a = tmem + TM_S + 128 * (j & 1);
                 if (j + 1 < nt && wait(dpfree, j & 1)) dprob(j + 1);
-                if (!ok || !wait(dsready, j & 1)) break;
+                // (two barriers: dP of the next tile is on its way, so the warps may be done with that one's dS before this
+                // one's arrival is seen; the one after next waits for S, which is issued below)
+                if (!ok || !wait(dsready0 + 8 * (j & 1), (j >> 1) & 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
                     tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 1) * 32 + (ks & 1) * 8, desc.mn(place(2 * j), ks), id_d,

@@ -261,6 +261,19 @@ def test_same_bits_on_every_run_and_stream():
         assert all(torch.equal(a, b) for a, b in zip(g, want))
 
 
+@pytest.mark.parametrize("T,H,HKV,D", [(4096, 32, 4, 128), (700, 16, 2, 128), (2100, 16, 4, 64)])
+def test_same_bits_over_many_runs(T, H, HKV, D):
+    """The warps of a CTA meet at barriers whose phases must not run ahead of a slow one: hundreds of launches of thousands
+    of CTAs, back to back."""
+    q, k, v, dout = heads(1, 1, T, H, D), heads(2, 1, T, HKV, D), heads(3, 1, T, HKV, D), heads(4, 1, T, H, D)
+    want = run(q, k, v, dout)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(150):
+        for a, b in zip(run(q, k, v, dout), want):
+            wrong += (a != b).sum()
+    assert wrong.item() == 0 and kda.device_error() == 0
+
+
 def test_captured_forward_and_backward_follow_new_inputs_and_lengths():
     """A graph of the pass replays on new values and new offsets of the same tensors."""
     T, H, HKV, D = 600, 4, 1, 128
