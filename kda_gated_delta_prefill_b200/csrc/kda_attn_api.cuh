@@ -137,9 +137,9 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
 
 namespace {
 
-// CTAs (a cluster) that share the query heads of a key tile: as long as they fill the SMs in one wave.  With fewer CTAs than
-// SMs a key tile's loop over all heads of its group is the longest chain there is; with more than a wave of them the clusters
-// cost more than they balance (D = 128, 32/8 heads; us per backward with 1, 2 and 4 CTAs):
+// CTAs (a cluster) that share the query heads of a key tile: as long as they fill the SMs in one wave.  With fewer CTAs
+// than SMs a key tile's loop over all heads of its group is the longest chain there is; with more than a wave of them
+// the clusters cost more than they balance (D = 128, 32/8 heads; us per backward with 1, 2 and 4 CTAs):
 //   512 tokens (32 key tiles): 41, 33, 32    1,024 (64): 69, 52, 60    2,048 (128): 133, 140, 161
 // and 8/1 heads, 2,048 tokens (16 key tiles): 232, 131, 72 and, with 8, 47.
 int backward_split(int group, int64_t units, int sms)
@@ -210,9 +210,11 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     p.dv = static_cast<__nv_bfloat16 *>(dv);
     p.err = info.err;
     CUtensorMap mq, mk, mv, mdo;
-    if (d.rows && (!attn_map(&mq, q, H, d.rows, q_row_stride, D) || !attn_map(&mdo, dout, H, d.rows, dout_row_stride, D)))
+    if (d.rows && (!attn_map(&mq, q, H, d.rows, q_row_stride, D) ||
+                   !attn_map(&mdo, dout, H, d.rows, dout_row_stride, D)))
         return KDA_ERR_CUDA;
-    if (d.krows && (!attn_map(&mk, k, HKV, d.krows, k_row_stride, D) || !attn_map(&mv, v, HKV, d.krows, v_row_stride, D)))
+    if (d.krows && (!attn_map(&mk, k, HKV, d.krows, k_row_stride, D) ||
+                    !attn_map(&mv, v, HKV, d.krows, v_row_stride, D)))
         return KDA_ERR_CUDA;
     // a side without rows: the kernels write zeros to the other side's gradients and load nothing
     if (!d.rows) mq = mdo = mk;
@@ -387,12 +389,13 @@ extern "C" kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, co
     p.HKV = HKV;
     p.num_blocks = num_blocks;
     p.err = info.err;
-    // Windows as small as leaves four waves of CTAs (8 of them fit an SM): one token for a step of requests, a block for
-    // prompts.  256 single tokens (8 heads, blocks of 64): 5 us with one warp a unit, 11 with four; prompts of 97,000 tokens
-    // (blocks of 16, where both are the same) do not differ.
+    // Windows as small as leaves 32 CTAs for each SM at most (3 fit at a time): one token for a step of requests, a
+    // block for prompts.  256 single tokens (8 heads, blocks of 64): 6 us with one warp a unit, 14 with four; prompts
+    // of 97,000 tokens (blocks of 16, where both are the same) do not differ.
     const int wpu = block_size / 16;
     const int64_t wide = (2ll * HKV * wpu + 7) / 8;  // CTAs of a run with BS / 16 warps a unit
-    p.window = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(1, T * wide / (32ll * info.sms))));
+    const int64_t fits = T * wide / (32ll * info.sms);
+    p.window = static_cast<int>(std::min<int64_t>(block_size, std::max<int64_t>(1, fits)));
     const bool few = p.window == 1;
     const int64_t grid = (T + p.window - 1ll) / p.window * (few ? (2ll * HKV + 7) / 8 : wide);
     if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
@@ -401,10 +404,11 @@ extern "C" kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, co
         constexpr bool F = decltype(fp8)::value;
         constexpr int DD = decltype(d)::value;
         auto run = [&](auto kern) { kern<<<static_cast<int>(grid), kAppendThreads, 0, s>>>(p); };
+        auto pick = [&](auto one, auto wide) { few ? run(one) : run(wide); };
         if (block_size == 16) run(kda_cache_append_kernel<F, DD, 16, 1>);
-        else if (block_size == 32) few ? run(kda_cache_append_kernel<F, DD, 32, 1>) : run(kda_cache_append_kernel<F, DD, 32, 2>);
-        else if (block_size == 64) few ? run(kda_cache_append_kernel<F, DD, 64, 1>) : run(kda_cache_append_kernel<F, DD, 64, 4>);
-        else few ? run(kda_cache_append_kernel<F, DD, 128, 1>) : run(kda_cache_append_kernel<F, DD, 128, 8>);
+        else if (block_size == 32) pick(kda_cache_append_kernel<F, DD, 32, 1>, kda_cache_append_kernel<F, DD, 32, 2>);
+        else if (block_size == 64) pick(kda_cache_append_kernel<F, DD, 64, 1>, kda_cache_append_kernel<F, DD, 64, 4>);
+        else pick(kda_cache_append_kernel<F, DD, 128, 1>, kda_cache_append_kernel<F, DD, 128, 8>);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
@@ -530,8 +534,8 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
             attr.id = cudaLaunchAttributeClusterDimension;
             attr.val.clusterDim.x = kAdCluster;
             attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            return launch(kda_attn_decode_kernel<F, DD, N, true>, static_cast<int>(units * kAdCluster), kAdThreads, smem, attr,
-                          mk, mv, shift);
+            return launch(kda_attn_decode_kernel<F, DD, N, true>, static_cast<int>(units * kAdCluster), kAdThreads, smem,
+                          attr, mk, mv, shift);
         }
         kda_status_t r = launch(kda_attn_decode_kernel<F, DD, N, false>, grid, kAdThreads, smem, attr, mk, mv, shift);
         if (r != KDA_OK) return r;

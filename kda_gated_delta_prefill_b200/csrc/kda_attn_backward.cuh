@@ -11,11 +11,11 @@
 // order: no atomics, the same bits every time.  The price is that S and dP are formed twice (7 matrix products
 // instead of 5).
 //
-// Precision.  P and dS are rounded to bf16 for the products (2^-9 relative), and delta inherits the rounding of o: where one
-// key has most of a row's probability, dP_ij - delta_i is a small difference of it.  dQ and dK are 2.5e-3 off for scores of
-// unit variance and up to 5e-3 where the softmax is all but one-hot (of the 2-norm; 1.7e-3 is bf16 results alone).
-// delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then has to follow dQ, and a
-// backward took 15-40 % longer.
+// Precision.  P and dS are rounded to bf16 for the products (2^-9 relative), and delta inherits the rounding of o:
+// where one key has most of a row's probability, dP_ij - delta_i is a small difference of it.  dQ and dK are 2.5e-3 off
+// for scores of unit variance and up to 5e-3 where the softmax is all but one-hot (of the 2-norm; 1.7e-3 is bf16
+// results alone). delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then
+// has to follow dQ, and a backward took 15-40 % longer.
 //
 // dK/dV works on the transposes: a thread owns a key row of S^T = K Q^T and dP^T = V dO^T, so P^T and dS^T go back to
 // TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
@@ -24,8 +24,9 @@
 // leaves two products' time for each of P (between S^T and dV) and dS (between dP^T and dK).
 //
 // The launches depend on one another on the device only as far as they have to: dK/dV sets up while the statistics are
-// formed, and dQ starts where SMs are idle at dK/dV's end (4,096 tokens, 16/4 heads: 345 -> 246 us).  Where key tiles are
-// few, a cluster of CTAs shares the heads of a group and adds up over distributed shared memory, in the CTAs' order.
+// formed, and dQ starts where SMs are idle at dK/dV's end (4,096 tokens, 16/4 heads: 345 -> 246 us).  Where key tiles
+// are few, a cluster of CTAs shares the heads of a group and adds up over distributed shared memory, in the CTAs'
+// order.
 #pragma once
 #include "kda_attn_common.cuh"
 
@@ -101,8 +102,9 @@ struct AttnDkvSmem {
     static constexpr int TOTAL = ABORT + 4;
 };
 // 16 warps of arithmetic (a quarter of the rows, 32 columns each), then one of MMAs, one of loads and two idle: five
-// warpgroups for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler and both
-// in the same step, most cycles issued nothing: TODO.
+// warpgroups for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler
+// and both in the same step, most cycles issued nothing: 133 -> 124 us for 2,048 tokens of 32/8 heads, 246 -> 229 for
+// 4,096 of 16/4.
 constexpr int kAttnBwdWarps = 16, kAttnBwdThreads = 32 * (kAttnBwdWarps + 4);
 constexpr int kAttnBwdMma = kAttnBwdWarps, kAttnBwdLoad = kAttnBwdWarps + 1;
 #define ATTN_BWD_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n")
@@ -245,8 +247,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else if (p.split > 1 && total > 0) {
-            // this CTA's sums over its heads, fp32, to shared memory: dV (groups 0, 1: half the columns each), dK (2, 3); nothing
-            // else uses the tiles any more
+            // this CTA's sums over its heads, fp32, to shared memory: dV (groups 0, 1: half the columns each), dK (2,
+            // 3); nothing else uses the tiles any more
             tc_fence_after();
             const int half = group >> 1, c0 = (group & 1) * (D / 2);
             const int row = 32 * quarter + lane;
@@ -275,13 +277,15 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     } else {
         ATTN_BWD_FEWER_REGISTERS();
         if (warp == kAttnBwdLoad + 1 && lane == 0) {
-            // (also in CTAs without work.)  The statistics are complete behind the wait, so dQ may start, where SMs are idle
+            // (also in CTAs without work.)  The statistics are complete behind the wait, so dQ may start, where SMs are
+            // idle
             asm volatile("griddepcontrol.wait;\n" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
         }
         if (warp == kAttnBwdLoad && lane == 0 && total > 0) {
             // ---------------- loads ----------------
-            asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the statistics (nothing else depends on that launch)
+            // the statistics (nothing else depends on that launch)
+            asm volatile("griddepcontrol.wait;\n" ::: "memory");
             int nqi = 0, ndo = 0;  // tiles of Q and of dO requested
             bool ok = true;
             auto tile = [&](const CUtensorMap *m, uint32_t dst, int head, int row, uint32_t bar) {
@@ -377,7 +381,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         cluster_sync();
         constexpr int Q4 = D / 4;
         const int rows = AT / p.split, r0 = rank * rows;
-        for (int i = tid; warp < kAttnBwdWarps && i < 2 * rows * Q4; i += 32 * kAttnBwdWarps) {  // (the other warps gave their registers away)
+        // (the arithmetic warps: the others gave their registers away)
+        for (int i = tid; warp < kAttnBwdWarps && i < 2 * rows * Q4; i += 32 * kAttnBwdWarps) {
             const int half = i / (rows * Q4), row = r0 + i / Q4 % rows, ch = i % Q4;
             const uint32_t at = sb + ((half * AT + row) * Q4 + (ch ^ (row & (Q4 - 1)))) * 16;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -404,7 +409,8 @@ struct AttnDqSmem {
     static constexpr int TILE = AT * D * 2;
     static constexpr int NST = D == 128 ? 5 : 8;
     static constexpr int RING = 2 * TILE;           // Q, dO, then K_0, V_0, K_1, V_1, ...
-    static constexpr int BAR = RING + NST * TILE;   // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready[2] done dpfree
+    // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready[2] done dpfree
+    static constexpr int BAR = RING + NST * TILE;
     static constexpr int TMEM_SLOT = BAR + (2 * NST + 9) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
@@ -424,8 +430,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
     int n, blk;
-    // dQ may start while dK/dV runs and has no use for it, but what follows in the stream waits for this launch only: the last
-    // CTA stays until dK/dV is complete
+    // dQ may start while dK/dV runs and has no use for it, but what follows in the stream waits for this launch only:
+    // the last CTA stays until dK/dV is complete
     auto linger = [] {
         if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");
     };
@@ -469,7 +475,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + blk;
         const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
         const float l2 = stat[r], delta = stat[AT + r];
-        const int seen = r0 + r + 1 + diff - 32 * group;  // keys of this group that the row sees (rows past the end: p = 0)
+        // keys of this group that the row sees (rows past the end: p = 0)
+        const int seen = r0 + r + 1 + diff - 32 * group;
         const float c = p.scale_log2;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
@@ -563,8 +570,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            auto place = [](int pos) { return S::RING + (pos % NST) * TILE; };  // ring positions: K_j at 2 j, V_j at 2 j + 1
-            // D[128 queries][128 keys] = (Q or dO) (K or V)^T, once the tile is there and what follows the sequence taken out
+            // ring positions: K_j at 2 j, V_j at 2 j + 1
+            auto place = [](int pos) { return S::RING + (pos % NST) * TILE; };
+            // D[128 queries][128 keys] = (Q or dO) (K or V)^T, once the tile is there and what follows the sequence
+            // taken out
             auto product = [&](uint32_t d, int rows, int pos, uint32_t commit) {
                 if (!wait(full0 + 8 * (pos % NST), (pos / NST) & 1)) return;
                 if (tail < AT && (pos >> 1) == nt - 1) zero_tail_rows<D>(sb + place(pos), tail, lane);
@@ -584,8 +593,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
                 const uint32_t a = tmem + TM_S + 128 * (j & 1);
                 if (j + 1 < nt && wait(dpfree, j & 1)) dprob(j + 1);
-                // (two barriers: dP of the next tile is on its way, so the warps may be done with that one's dS before this
-                // one's arrival is seen; the one after next waits for S, which is issued below)
+                // (two barriers: dP of the next tile is on its way, so the warps may be done with that one's dS before
+                // this one's arrival is seen; the one after next waits for S, which is issued below)
                 if (!ok || !wait(dsready0 + 8 * (j & 1), (j >> 1) & 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)

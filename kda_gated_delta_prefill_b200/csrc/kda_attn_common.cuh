@@ -10,8 +10,8 @@ namespace kda {
 // further bits of the device error word
 enum : unsigned { ERR_BLOCK_ID = 16u, ERR_CACHE_FULL = 32u };
 
-// Wait for a phase without taking issue slots from the scheduler's other warps: mbarrier.try_wait suspends the warp for a
-// time that the hardware chooses (with a long limit of one's own it also resumes late).  Bounded like mbar_wait.
+// Wait for a phase without taking issue slots from the scheduler's other warps: mbarrier.try_wait suspends the warp for
+// a time that the hardware chooses (with a long limit of one's own it also resumes late).  Bounded like mbar_wait.
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -230,8 +230,8 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, 
     }
 }
 
-// The sequence and block of the t-th CTA (of block_slots<BLK>()), those with most work first: blocks in levels by their place
-// in their sequence, the last ones first (LAST) or the first ones.  With up to 128 packed sequences a warp holds
+// The sequence and block of the t-th CTA (of block_slots<BLK>()), those with most work first: blocks in levels by their
+// place in their sequence, the last ones first (LAST) or the first ones.  With up to 128 packed sequences a warp holds
 // their block counts and searches for the level; with more, blocks go in the order of their slots.
 template <int BLK, bool LAST>
 __device__ __forceinline__ bool pick_block(const int32_t *cu, int N, int T, int t, int lane, int &n, int &blk)

@@ -5,12 +5,13 @@
 // key/value head.
 //
 // The work is cut evenly over the CTAs, whatever the lengths: the tiles of 64 tokens of all (row, key/value head)
-// units stand in one line of W, and CTA c of G <= W takes tiles [c W / G, (c + 1) W / G) of it.  A unit inside one CTA is
-// finished there; of a unit that several CTAs share, each leaves its maximum, sum and accumulator, and a second, dependent
-// launch joins them in the order of the CTAs.
+// units stand in one line of W, and CTA c of G <= W takes tiles [c W / G, (c + 1) W / G) of it.  A unit inside one CTA
+// is finished there; of a unit that several CTAs share, each leaves its maximum, sum and accumulator, and a second,
+// dependent launch joins them in the order of the CTAs.
 //
-// Few short requests take another form: a cluster of eight CTAs per unit, which join over distributed shared memory, with
-// no scan of the lengths and no second launch (one request of 777 tokens, 32/8 heads: 5.8 us on the device, 8.9 in the other).
+// Few short requests take another form: a cluster of eight CTAs per unit, which join over distributed shared memory,
+// with no scan of the lengths and no second launch (one request of 777 tokens, 32/8 heads: 5.8 us on the device, 8.9 in
+// the other).
 //
 // In a CTA, one warp requests the tiles' pages by TMA through a ring; four warps take 16 tokens of a tile each, with a
 // running softmax of their own, and join at the end of the unit.  All query heads of a group share one pass over the
@@ -20,8 +21,8 @@
 // tcgen05 would want the codes in shared memory as fp16, and at 24 bytes per cycle and SM mma.sync is not what bounds.
 //
 // The value scale goes into the exponent: with t_j = s_j log2(e) + log2(vs_b), the weights p_j = 2^(t_j - M) are
-// what multiplies the codes and p_j / vs_b is what the softmax's sum adds.  M is a running reference of t, so a weight is
-// small only where its product with the codes is.  Weights are fp16 (11 bits), 2^12 at the reference and at most
+// what multiplies the codes and p_j / vs_b is what the softmax's sum adds.  M is a running reference of t, so a weight
+// is small only where its product with the codes is.  Weights are fp16 (11 bits), 2^12 at the reference and at most
 // 2^15, which keeps what is flushed below 2^-37 of the largest.
 #pragma once
 #include "kda_attn_common.cuh"
@@ -31,12 +32,14 @@ namespace kda {
 
 // A tile is 16 KB of codes: 64 tokens at D = 128, 128 at D = 64, where a warp takes two slices of 16 tokens at once.
 // The warps' work on a tile is a chain of latencies (shared memory, MMAs, shuffles, exponentials, MMAs), so three CTAs
-// share an SM where registers allow it (up to 8 query heads): TODO measured.
+// share an SM where registers allow it (up to 8 query heads): 161 -> 147 us for 512 int8 requests of up to 4,096
+// tokens.
 __host__ __device__ constexpr int ad_tile(int D) { return 64 * (128 / D); }
 __host__ __device__ constexpr int ad_ctas(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
 // The form for few short requests: CTAs of a unit, and the most tiles that its table may hold (one request, 32/8 heads,
-// D = 128; us on the device with a cluster and without: 500 tokens 5.4, 8.5; 2,000: 7.1, 10.2; 8,000: 13, 15; 32,000: 37, 21).
+// D = 128; us on the device with a cluster and without: 500 tokens 5.4, 8.5; 2,000: 7.1, 10.2; 8,000: 13, 15; 32,000:
+// 37, 21).
 constexpr int kAdCluster = 8, kAdClusterTiles = 128;
 
 struct AttnDecodeParams {
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
 {
     using S = AttnDecodeSmem<D, NT>;
     constexpr int NST = S::NST, HB = S::HB, HALF = S::HALF, SL = S::SL, KS = D / 16, MT = D / 16;
-    constexpr int TILE = ad_tile(D), SLICES = TILE / 16, BATCH = 32 / SLICES;  // tiles whose pages the loader looks up at once
+    constexpr int TILE = ad_tile(D), SLICES = TILE / 16, BATCH = 32 / SLICES;  // (tiles looked up at once)
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -608,8 +611,8 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
 }
 
 // Joins the pieces of a unit that began in CTA c, in their order.  A thread takes a head, four dims and a run of the
-// pieces; the runs are joined through shared memory.  Bound by the latency of its dependent loads (which unit; references
-// and accumulators, eight pieces at a time).
+// pieces; the runs are joined through shared memory.  Bound by the latency of its dependent loads (which unit;
+// references and accumulators, eight pieces at a time).
 constexpr int kAdJoinThreads = 512;
 struct AttnPiece {
     float M, l;

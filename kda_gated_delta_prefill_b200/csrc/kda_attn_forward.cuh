@@ -13,19 +13,19 @@
 //   warps 0-3, 4-7  softmax of tile A, B: a thread per row
 //   warp 8 (and 9)  issues the MMAs: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM)
 //   warp 10         TMA loads of Q, and of K and V tiles through a ring
-// TMEM: S_A, S_B (128 columns each), O_A, O_B and, where there is room (D = 64), P_A and P_B.  P is handed over in halves
-// of 64 keys, so that O += P V starts while the second half is formed (at D = 128: 4.07 -> 3.46 ms for 32,768 tokens and 16
-// heads).
-//  D = 128: P lies over S, so S of the next key tile is issued behind O += P V of this one, and one warp issues for both
-//    tiles in turn, which keeps them half a period apart: while one is in its softmax, the tensor cores work on the other.
-//    A softmax warp that sees S may also rescale O: no MMA writes it then.
-//  D = 64: S of the next key tile is issued as soon as the softmax has read this one into registers, and each tile has its
-//    own issuer (0.69-0.75 ms for 16,384 tokens and 16 heads; 0.83 with P over S).
-// Bound at D = 64 by the exponentials (16 a cycle and SM: 2,048 cycles for both tiles, of about 2,700), and at D = 128, for
-// long sequences, by power: at 1,340 TFLOP/s the clock falls to 1.6 GHz.  Measured there without gain: a polynomial on the
-// FMA pipe for a quarter of the exponentials; scores in halves with N = 64, so that neither waits for the other (fewer
-// cycles, but Q read twice: less clock, 3.86 ms).  Waiting warps are suspended (mbarrier.try_wait): polling took issue slots
-// from the softmax (3.46 -> 3.36 ms).
+// TMEM: S_A, S_B (128 columns each), O_A, O_B and, where there is room (D = 64), P_A and P_B.  P is handed over in
+// halves of 64 keys, so that O += P V starts while the second half is formed (at D = 128: 4.07 -> 3.46 ms for 32,768
+// tokens and 16 heads).
+//  D = 128: P lies over S, so S of the next key tile is issued behind O += P V of this one, and one warp issues for
+//    both tiles in turn, which keeps them half a period apart: while one is in its softmax, the tensor cores work on
+//    the other. A softmax warp that sees S may also rescale O: no MMA writes it then.
+//  D = 64: S of the next key tile is issued as soon as the softmax has read this one into registers, and each tile has
+//    its own issuer (0.69-0.75 ms for 16,384 tokens and 16 heads; 0.83 with P over S).
+// Bound at D = 64 by the exponentials (16 a cycle and SM: 2,048 cycles for both tiles, of about 2,700), and at D = 128,
+// for long sequences, by power: at 1,340 TFLOP/s the clock falls to 1.6 GHz.  Measured there without gain: a polynomial
+// on the FMA pipe for a quarter of the exponentials; scores in halves with N = 64, so that neither waits for the other
+// (fewer cycles, but Q read twice: less clock, 3.86 ms).  Waiting warps are suspended (mbarrier.try_wait): polling took
+// issue slots from the softmax (3.46 -> 3.36 ms).
 #pragma once
 #include <type_traits>
 
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             }
             l += (sum.x + sum.y) + (sum1.x + sum1.y);
         }
-        // ---------------- o = O / l, through this warp's rows of the Q tile (no MMA reads it any more) ----------------
+        // ---------------- o = O / l, through this warp's rows of the Q tile ----------------
         if (ok && nt[w] > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(odone0 + 8 * w, kOwnP ? (nt[w] - 1) & 1 : 0));
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                 };
                 // ring positions: K_j at 2 j, V_j at 2 j + 1
                 auto arrived = [&](int pos) { return wait(full0 + 8 * (pos % NST), (pos / NST) & 1); };
-                // An issuer lets go of every position, also of those that its tile does not use, but of none before it is
-                // there: an arrival ahead of the loads would count for the position's predecessor in the ring.
+                // An issuer lets go of every position, also of those that its tile does not use, but of none before it
+                // is there: an arrival ahead of the loads would count for the position's predecessor in the ring.
                 auto release = [&](int pos) {
                     if (arrived(pos)) tc_commit_warp(empty0 + 8 * (pos % NST));
                 };

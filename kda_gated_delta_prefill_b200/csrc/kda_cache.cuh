@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
             p.block_table[b * p.table_stride + k] = f < p.num_free ? p.free_blocks[f] : -1;
         }
     }
-    // The slot of each token; -1 behind the last one, and where there is no block.  A thread takes four tokens: one search
-    // and one table entry, unless a row or a block ends among them.
+    // The slot of each token; -1 behind the last one, and where there is no block.  A thread takes four tokens: one
+    // search and one table entry, unless a row or a block ends among them.
     int steps = 0;
     while ((1 << steps) < p.B) ++steps;
     const bool wide = (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0;
