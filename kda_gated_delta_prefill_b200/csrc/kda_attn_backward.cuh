@@ -40,7 +40,7 @@ struct AttnBwdParams {
     const __nv_bfloat16 *o, *dout;
     int64_t do_stride;
     const float *lse;
-    float *stats;  // [H][qslots][2][128]: lse * log2(e) (+inf: no probability), delta
+    float *stats;  // [H][qslots][2][128]: -lse * log2(e) (-inf: no probability), -delta
     __nv_bfloat16 *dq, *dk, *dv;
     unsigned *err;
 };
@@ -75,14 +75,14 @@ __global__ void __launch_bounds__(kAttnStatThreads) kda_attn_stats_kernel(const 
 #pragma unroll
         for (int off = LPR / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         if (lane % LPR == 0) {
-            float l2 = INFINITY;
+            float l2 = -INFINITY;
             if (row < sq.lq) {
                 const int64_t at = p.seq.cu_q ? static_cast<int64_t>(h) * p.seq.T + sq.q0 + row
                                               : (static_cast<int64_t>(n) * p.H + h) * p.seq.T + row;
-                l2 = p.lse[at] == -INFINITY ? INFINITY : p.lse[at] * kLog2e;
+                l2 = p.lse[at] == -INFINITY ? -INFINITY : -p.lse[at] * kLog2e;
             }
             out[r] = l2;
-            out[AT + r] = s;
+            out[AT + r] = -s;
         }
     }
 }
@@ -104,7 +104,9 @@ struct AttnDkvSmem {
 // 16 warps of arithmetic (a quarter of the rows, 32 columns each), then one of MMAs, one of loads and two idle: five
 // warpgroups for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler
 // and both in the same step, most cycles issued nothing: 133 -> 124 us for 2,048 tokens of 32/8 heads, 246 -> 229 for
-// 4,096 of 16/4.
+// 4,096 of 16/4.  The statistics of the 32 columns are read from shared memory ahead of the scores and of dP, not behind
+// them (the MMAs take most of its bandwidth): with them stored negated and masks set in a branch of their own, 134 ->
+// 127 us and 173 -> 166 us (4,096 tokens, 16/16 heads, D = 64).
 constexpr int kAttnBwdWarps = 16, kAttnBwdThreads = 32 * (kAttnBwdWarps + 4);
 constexpr int kAttnBwdMma = kAttnBwdWarps, kAttnBwdLoad = kAttnBwdWarps + 1;
 #define ATTN_BWD_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n")
@@ -176,40 +178,39 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const int key = j0 + 32 * quarter + lane;
         const float c = p.scale_log2;
         bool ok = true;
-        for (int it = 0; it < total; ++it) {
-            const int i = first + it % cnt, st = it % NST;
-            ok = mbar_wait_quiet(qfull + 8 * st, (it / NST) & 1) && mbar_wait_quiet(sfull, it & 1);
-            ok = __all_sync(0xffffffffu, ok);
+        // queries q >= key - diff see the key; counted from this warp's first column of tile i
+        const int seen = key - diff - 32 * group;
+        for (int it = 0, i = first; it < total; ++it, i = i + 1 == nq ? first : i + 1) {
+            const int st = it % NST;
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(qfull + 8 * st, (it / NST) & 1));
+            if (!ok) break;
+            const float4 *stat = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 8 * group;
+            float4 l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l[e] = stat[e];
+            ok = __all_sync(0xffffffffu, mbar_wait_quiet(sfull, it & 1));
             if (!ok) break;
             tc_fence_after();
             uint32_t r[32];
             tc_ld32(ts, r);
-            const float4 *l2 = reinterpret_cast<const float4 *>(sm + S::STAT + st * 1024) + 8 * group;
-            const float4 *dl = l2 + 32;
             tc_wait_ld();
             if (kOwn) arrive(sfree);
-            // queries q >= key - diff see the key
-            const int from = key - diff - i * AT - 32 * group;
-            const bool cut = __any_sync(0xffffffffu, from > 0);
+            const int from = seen - i * AT;
+            if (__any_sync(0xffffffffu, from > 0)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e < from) r[e] = 0xff800000u;  // -inf
+            }
             float2 pr[16];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float4 l = l2[e];
                 const uint32_t *x = &r[4 * e];
-                float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c, c),
-                                make_float2(-l.x, -l.y));
-                float2 b = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c, c),
-                                make_float2(-l.z, -l.w));
-                a = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
-                b = make_float2(ex2_ftz(b.x), ex2_ftz(b.y));
-                if (cut) {
-                    if (4 * e < from) a.x = 0.f;
-                    if (4 * e + 1 < from) a.y = 0.f;
-                    if (4 * e + 2 < from) b.x = 0.f;
-                    if (4 * e + 3 < from) b.y = 0.f;
-                }
-                pr[2 * e] = a;
-                pr[2 * e + 1] = b;
+                const float2 a = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), make_float2(c, c),
+                                      make_float2(l[e].x, l[e].y));
+                const float2 b = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), make_float2(c, c),
+                                      make_float2(l[e].z, l[e].w));
+                pr[2 * e] = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
+                pr[2 * e + 1] = make_float2(ex2_ftz(b.x), ex2_ftz(b.y));
             }
             ok = reusable(doempty, it);
             if (!ok) break;
@@ -220,25 +221,31 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             tc_wait_st();
             arrive(pready);
 
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l[e] = stat[32 + e];
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, it & 1));
             if (!ok) break;
             tc_fence_after();
-            tc_ld32(td, r);
-            tc_wait_ld();
-            if (kOwn) arrive(dpfree);
-            ok = reusable(qempty, it);
-            if (!ok) break;
+            // (in halves: fewer registers)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 d4 = dl[e];
-                const uint32_t *x = &r[4 * e];
-                const float2 a = mul2(pr[2 * e], add2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                                      make_float2(-d4.x, -d4.y)));
-                const float2 b = mul2(pr[2 * e + 1], add2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                                          make_float2(-d4.z, -d4.w)));
-                w[2 * e] = pack_bf16(a.x, a.y);
-                w[2 * e + 1] = pack_bf16(b.x, b.y);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t x[16];
+                tc_ld16(td + 16 * half, x);
+                tc_wait_ld();
+                if (half == 1) {
+                    if (kOwn) arrive(dpfree);
+                    ok = reusable(qempty, it);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 d4 = l[4 * half + e / 2];
+                    const float2 a = mul2(pr[8 * half + e],
+                                          add2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                               e & 1 ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
+                    w[8 * half + e] = pack_bf16(a.x, a.y);
+                }
             }
+            if (!ok) break;
             tc_st16(tds, w);
             tc_wait_st();
             arrive(dsready);
@@ -293,8 +300,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             };
             mbar_expect_tx(kfull, TILE);
             tile(&mk, sb, hk, sq.k0 + j0, kfull);
-            for (int it = 0; it < total && ok && !*abort_flag; ++it) {
-                const int hq = head0 + it / cnt, i = first + it % cnt, st = it % NST;
+            for (int it = 0, hq = head0, i = first; it < total && ok && !*abort_flag; ++it) {
+                const int st = it % NST;
                 const uint32_t par = ((it / NST) - 1) & 1;
                 if (it >= NST && !mbar_wait(qempty + 8 * st, par)) {
                     ok = false;
@@ -316,6 +323,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 mbar_expect_tx(dofull + 8 * st, TILE);
                 tile(&mdo, sb + S::DO + st * TILE, hq, sq.q0 + i * AT, dofull + 8 * st);
                 ++ndo;
+                if (++i == nq) {
+                    i = first;
+                    ++hq;
+                }
             }
             if (!ok) fail(ERR_PIPE_EMPTY_WAIT);
             if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
@@ -336,17 +347,21 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 return ok;
             };
             // D[128 keys][128 queries] = (K or V) (Q or dO)^T of iteration it, once the tile is there
-            auto product = [&](uint32_t d, int keys, int ring, uint32_t full, uint32_t commit, int it) {
+            auto product = [&](uint32_t d, int keys, int ring, uint32_t full, uint32_t commit, int it, int &left) {
                 const int st = it % NST, at = ring + st * TILE;
                 if (!wait(full + 8 * st, (it / NST) & 1)) return;
-                if (tail < AT && it % cnt == cnt - 1) zero_tail_rows<D>(sb + at, tail, lane);
+                if (--left == 0) {  // the last tile of a head
+                    left = cnt;
+                    if (tail < AT) zero_tail_rows<D>(sb + at, tail, lane);
+                }
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     tc_mma_ss_warp(d, desc.k(keys, ks), desc.k(at, ks), id_s, ks > 0);
                 tc_commit_warp(commit);
             };
-            auto score = [&](int it) { product(tmem + TM_S, 0, S::Q, qfull, sfull, it); };
-            auto dprob = [&](int it) { product(tmem + TM_DP, TILE, S::DO, dofull, dpfull, it); };
+            int left_q = cnt, left_do = cnt;
+            auto score = [&](int it) { product(tmem + TM_S, 0, S::Q, qfull, sfull, it, left_q); };
+            auto dprob = [&](int it) { product(tmem + TM_DP, TILE, S::DO, dofull, dpfull, it, left_do); };
             // D += A B, A in groups of 32 queries
             auto accumulate = [&](uint32_t d, uint32_t a, int at, bool more) {
 #pragma unroll
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const int r = 32 * quarter + lane;
         const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + blk;
         const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
-        const float l2 = stat[r], delta = stat[AT + r];
+        const float2 l2 = make_float2(stat[r], stat[r]), delta = make_float2(stat[AT + r], stat[AT + r]);
         // keys of this group that the row sees (rows past the end: p = 0)
         const int seen = r0 + r + 1 + diff - 32 * group;
         const float c = p.scale_log2;
@@ -488,18 +503,17 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             tc_ld32(ts, x);
             tc_wait_ld();
             const int keys = seen - j * AT;
-            const bool cut = __any_sync(0xffffffffu, keys < 32);
+            if (__any_sync(0xffffffffu, keys < 32)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e >= keys) x[e] = 0xff800000u;  // -inf
+            }
             float2 pr[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                float2 a = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                make_float2(c, c), make_float2(-l2, -l2));
-                a = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
-                if (cut) {
-                    if (2 * e >= keys) a.x = 0.f;
-                    if (2 * e + 1 >= keys) a.y = 0.f;
-                }
-                pr[e] = a;
+                const float2 a = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                      make_float2(c, c), l2);
+                pr[e] = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
             }
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, j & 1));
             if (!ok) break;
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 a = mul2(pr[e], add2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                                  make_float2(-delta, -delta)));
+                                                  delta));
                 w[e] = pack_bf16(a.x, a.y);
             }
             tc_st16(ts, w);
