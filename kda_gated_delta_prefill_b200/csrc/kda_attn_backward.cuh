@@ -21,7 +21,11 @@
 // TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
 // TMEM (D = 128): S^T/P^T, dP^T/dS^T, dV, dK with 128 columns each.  The order of the MMAs,
 //   dV(i), S^T(i+1), dK(i), dP^T(i+1), dV(i+1), ...
-// leaves two products' time for each of P (between S^T and dV) and dS (between dP^T and dK).
+// leaves two products' time for each of P (between S^T and dV) and dS (between dP^T and dK).  At D = 64, where P and dS
+// have columns of their own, S^T of the next tile does not wait for dV, and one issuing warp was what everything waited
+// for (a wait costs it 120 cycles and an MMA 40): two warps issue, S^T and dV the one, dP^T and dK the other, so every
+// sum still has one order (8,192 tokens, 16/16 heads: 327 -> 291 us).  At D = 128 that is slower (1,600 -> 1,750 us for
+// 16,384 tokens of 16/4 heads): dP and dK come between dV and S, which are the longest chain.
 //
 // The launches depend on one another on the device only as far as they have to: dK/dV sets up while the statistics are
 // formed, and dQ starts where SMs are idle at dK/dV's end (4,096 tokens, 16/4 heads: 345 -> 246 us).  Where key tiles
@@ -101,14 +105,14 @@ struct AttnDkvSmem {
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
-// 16 warps of arithmetic (a quarter of the rows, 32 columns each), then one of MMAs, one of loads and two idle: five
-// warpgroups for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler
-// and both in the same step, most cycles issued nothing: 133 -> 124 us for 2,048 tokens of 32/8 heads, 246 -> 229 for
-// 4,096 of 16/4.  The statistics of the 32 columns are read from shared memory ahead of the scores and of dP, not behind
-// them (the MMAs take most of its bandwidth): with them stored negated and masks set in a branch of their own, 134 ->
-// 127 us and 173 -> 166 us (4,096 tokens, 16/16 heads, D = 64).
+// 16 warps of arithmetic (a quarter of the rows, 32 columns each), then two of MMAs and one of loads: five warpgroups
+// for the register split (512 * 104 + 128 * 64 = 640 * 96).  With 8 warps of 64 columns, two on a scheduler and both in
+// the same step, most cycles issued nothing: 133 -> 124 us for 2,048 tokens of 32/8 heads, 246 -> 229 for 4,096 of
+// 16/4.  The statistics of the 32 columns are read from shared memory ahead of the scores and of dP, not behind them
+// (the MMAs take most of its bandwidth): with them stored negated and masks set in a branch of their own, 134 -> 127 us
+// and 173 -> 166 us (4,096 tokens, 16/16 heads, D = 64).
 constexpr int kAttnBwdWarps = 16, kAttnBwdThreads = 32 * (kAttnBwdWarps + 4);
-constexpr int kAttnBwdMma = kAttnBwdWarps, kAttnBwdLoad = kAttnBwdWarps + 1;
+constexpr int kAttnBwdMma = kAttnBwdWarps, kAttnBwdLoad = kAttnBwdWarps + 2;  // two warps issue MMAs
 #define ATTN_BWD_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n")
 #define ATTN_BWD_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n")
 
@@ -120,7 +124,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 {
     using S = AttnDkvSmem<D>;
     constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
-    constexpr bool kOwn = D == 64;  // P and dS have columns of their own
+    constexpr bool kOwn = D == 64;           // P and dS have columns of their own
+    constexpr int kIssuers = kOwn ? 2 : 1;  // warps that issue MMAs
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
     constexpr uint32_t TM_P = kOwn ? 384 : TM_S, TM_DS = kOwn ? 448 : TM_DP, TM_GROUP = kOwn ? 16 : 32;  // 32 queries
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -142,8 +147,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                    dpfull = kfull + 32, dsready = kfull + 40, done = kfull + 48, sfree = kfull + 56, dpfree = kfull + 64;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
-        for (int s = 0; s < 4 * NST; ++s) mbar_init(qfull + 8 * s, 1);
-        for (uint32_t b : {kfull, vfull, sfull, dpfull, done}) mbar_init(b, 1);
+        for (int s = 0; s < 3 * NST; ++s) mbar_init(qfull + 8 * s, 1);
+        for (int s = 0; s < NST; ++s) mbar_init(doempty + 8 * s, kIssuers);  // dP and dV are done with the tile
+        for (uint32_t b : {kfull, vfull, sfull, dpfull}) mbar_init(b, 1);
+        mbar_init(done, kIssuers);
         for (uint32_t b : {pready, dsready, sfree, dpfree}) mbar_init(b, kAttnBwdWarps);
         *abort_flag = 0;
         fence_mbar_init();
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 for (int i = max(0, nqi - NST); i < nqi; ++i) mbar_wait(qfull + 8 * (i % NST), (i / NST) & 1);
                 for (int i = max(0, ndo - NST); i < ndo; ++i) mbar_wait(dofull + 8 * (i % NST), (i / NST) & 1);
             }
-        } else if (warp == kAttnBwdMma && total > 0) {
+        } else if (warp < kAttnBwdMma + kIssuers && total > 0) {
             // ---------------- MMAs ----------------
             constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
             const TileDesc desc(sb);
@@ -346,43 +353,75 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            // D[128 keys][128 queries] = (K or V) (Q or dO)^T of iteration it, once the tile is there
-            auto product = [&](uint32_t d, int keys, int ring, uint32_t full, uint32_t commit, int it, int &left) {
-                const int st = it % NST, at = ring + st * TILE;
-                if (!wait(full + 8 * st, (it / NST) & 1)) return;
-                if (--left == 0) {  // the last tile of a head
+            // the tile of iteration it of a ring, once it is there; left: tiles to the end of its head
+            auto arrived = [&](uint32_t full, int ring, int it, int &left) {
+                const int st = it % NST;
+                if (!wait(full + 8 * st, (it / NST) & 1)) return false;
+                if (--left == 0) {
                     left = cnt;
-                    if (tail < AT) zero_tail_rows<D>(sb + at, tail, lane);
+                    if (tail < AT) zero_tail_rows<D>(sb + ring + st * TILE, tail, lane);
                 }
+                return true;
+            };
+            // D[128 keys][128 queries] = (K or V) (Q or dO)^T
+            auto product = [&](uint32_t d, int keys, int at, uint32_t commit) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     tc_mma_ss_warp(d, desc.k(keys, ks), desc.k(at, ks), id_s, ks > 0);
                 tc_commit_warp(commit);
             };
-            int left_q = cnt, left_do = cnt;
-            auto score = [&](int it) { product(tmem + TM_S, 0, S::Q, qfull, sfull, it, left_q); };
-            auto dprob = [&](int it) { product(tmem + TM_DP, TILE, S::DO, dofull, dpfull, it, left_do); };
             // D += A B, A in groups of 32 queries
             auto accumulate = [&](uint32_t d, uint32_t a, int at, bool more) {
 #pragma unroll
                 for (int ks = 0; ks < AT / 16; ++ks)
                     tc_mma_ts_warp(d, a + (ks >> 1) * TM_GROUP + (ks & 1) * 8, desc.mn(at, ks), id_d, more || ks > 0);
             };
-            if (wait(kfull, 0)) score(0);
-            if (wait(vfull, 0)) dprob(0);
-            for (int it = 0; it < total && ok && !__any_sync(0xffffffffu, *abort_flag); ++it) {
-                const int st = it % NST;
-                const bool more = it + 1 < total;
-                if (kOwn && more && wait(sfree, it & 1)) score(it + 1);
-                if (!ok || !wait(pready, it & 1)) break;
-                accumulate(tmem + TM_DV, tmem + TM_P, S::DO + st * TILE, it > 0);
-                tc_commit_warp(doempty + 8 * st);
-                if (!kOwn && more) score(it + 1);
-                if (kOwn && more && wait(dpfree, it & 1)) dprob(it + 1);
-                if (!ok || !wait(dsready, it & 1)) break;
-                accumulate(tmem + TM_DK, tmem + TM_DS, S::Q + st * TILE, it > 0);
-                tc_commit_warp(qempty + 8 * st);
-                if (!kOwn && more) dprob(it + 1);
+            int left = cnt, left_do = cnt;
+            auto score = [&](int it) {
+                if (arrived(qfull, S::Q, it, left)) product(tmem + TM_S, 0, S::Q + (it % NST) * TILE, sfull);
+            };
+            auto dprob = [&](int it) {
+                if (!arrived(dofull, S::DO, it, left_do)) return;
+                product(tmem + TM_DP, TILE, S::DO + (it % NST) * TILE, dpfull);
+                if (kIssuers == 2) tc_commit_warp(doempty + 8 * (it % NST));  // (else dV's commit covers it)
+            };
+            auto dv = [&](int it) {
+                accumulate(tmem + TM_DV, tmem + TM_P, S::DO + (it % NST) * TILE, it > 0);
+                tc_commit_warp(doempty + 8 * (it % NST));
+            };
+            auto dk = [&](int it) {
+                accumulate(tmem + TM_DK, tmem + TM_DS, S::Q + (it % NST) * TILE, it > 0);
+                tc_commit_warp(qempty + 8 * (it % NST));
+            };
+            auto go = [&](int it) { return it < total && ok && !__any_sync(0xffffffffu, *abort_flag); };
+            if (!kOwn) {
+                if (wait(kfull, 0)) score(0);
+                if (wait(vfull, 0)) dprob(0);
+                for (int it = 0; go(it); ++it) {
+                    const bool more = it + 1 < total;
+                    if (!wait(pready, it & 1)) break;
+                    dv(it);
+                    if (more) score(it + 1);
+                    if (!ok || !wait(dsready, it & 1)) break;
+                    dk(it);
+                    if (more) dprob(it + 1);
+                }
+            } else if (warp == kAttnBwdMma) {  // S and dV
+                if (wait(kfull, 0)) score(0);
+                for (int it = 0; go(it); ++it) {
+                    if (it + 1 < total && wait(sfree, it & 1)) score(it + 1);
+                    // (dO's tile for this warp too: the other may not be there yet)
+                    if (!ok || !arrived(dofull, S::DO, it, left_do) || !wait(pready, it & 1)) break;
+                    dv(it);
+                }
+            } else {  // dP and dK
+                if (wait(vfull, 0)) dprob(0);
+                for (int it = 0; go(it); ++it) {
+                    if (it + 1 < total && wait(dpfree, it & 1)) dprob(it + 1);
+                    // (S of this tile is complete: what follows the sequence in Q is zero)
+                    if (!ok || !wait(qfull + 8 * (it % NST), (it / NST) & 1) || !wait(dsready, it & 1)) break;
+                    dk(it);
+                }
             }
             tc_commit_warp(done);
             if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
@@ -418,15 +457,17 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 // ---------------------------------------------------------------------------------------------------- dQ
 // One CTA per tile of 128 queries of a head; a thread owns a query row of S and dP.  TMEM: S in two buffers (dS in
 // bf16 over the one it came from), dP, dQ.  S of the next key tile is formed while this one's exponentials run, and
-// dP of the next while P of the next is formed.
+// dP of the next while P of the next is formed.  Two warps issue MMAs, S and dP the one and dQ the other, and K and V
+// have rings of their own, as V's tiles are done with earlier: 1,340 -> 1,190 us (16,384 tokens, 16/4 heads), 266 ->
+// 242 (8,192 tokens, 16/16 heads, D = 64) against one warp and one ring.
 template <int D>
 struct AttnDqSmem {
     static constexpr int TILE = AT * D * 2;
-    static constexpr int NST = D == 128 ? 5 : 8;
-    static constexpr int RING = 2 * TILE;           // Q, dO, then K_0, V_0, K_1, V_1, ...
-    // full[NST] empty[NST] qfull dofull sfull[2] dpfull dsready[2] done dpfree
-    static constexpr int BAR = RING + NST * TILE;
-    static constexpr int TMEM_SLOT = BAR + (2 * NST + 9) * 8;
+    static constexpr int NK = D == 128 ? 3 : 4, NV = D == 128 ? 2 : 4;
+    static constexpr int K = 2 * TILE, V = K + NK * TILE;  // Q, dO, then the rings of K and V
+    // kfull[NK] kempty[NK] vfull[NV] vempty[NV] qfull dofull sfull[2] dpfull dsready[2] done dpfree
+    static constexpr int BAR = V + NV * TILE;
+    static constexpr int TMEM_SLOT = BAR + (2 * (NK + NV) + 9) * 8;
     static constexpr int ABORT = TMEM_SLOT + 4;
     static constexpr int TOTAL = ABORT + 4;
 };
@@ -438,7 +479,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                        const __grid_constant__ CUtensorMap mdo)
 {
     using S = AttnDqSmem<D>;
-    constexpr int NST = S::NST, TILE = S::TILE, HALVES = D / 64;
+    constexpr int NK = S::NK, NV = S::NV, TILE = S::TILE, HALVES = D / 64;
     constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384, TM_COLS = 512;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
@@ -459,12 +500,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int seen_tile = min(r0 + AT, sq.lq) + diff;  // keys that the tile's last row sees
     const int nt = seen_tile <= 0 ? 0 : (seen_tile + AT - 1) / AT;
 
-    const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull = empty0 + 8 * NST, dofull = qfull + 8,
-                   sfull0 = qfull + 16, dpfull = qfull + 32, dsready0 = qfull + 40, done = qfull + 56, dpfree = qfull + 64;
+    const uint32_t kfull = sb + S::BAR, kempty = kfull + 8 * NK, vfull = kempty + 8 * NK, vempty = vfull + 8 * NV,
+                   qfull = vempty + 8 * NV, dofull = qfull + 8, sfull0 = qfull + 16, dpfull = qfull + 32, dsready0 = qfull + 40, done = qfull + 56, dpfree = qfull + 64;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);
     if (tid == 0) {
-        for (int s = 0; s < 2 * NST; ++s) mbar_init(full0 + 8 * s, 1);
-        for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull, done}) mbar_init(b, 1);
+        for (int s = 0; s < 2 * (NK + NV); ++s) mbar_init(kfull + 8 * s, 1);
+        for (uint32_t b : {qfull, dofull, sfull0, sfull0 + 8, dpfull}) mbar_init(b, 1);
+        mbar_init(done, 2);
         for (int b = 0; b < 2; ++b) mbar_init(dsready0 + 8 * b, kAttnBwdWarps);
         mbar_init(dpfree, kAttnBwdWarps);
         *abort_flag = 0;
@@ -557,24 +599,31 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 for (int c = 0; c < HALVES; ++c) tma_load_3d(dst + c * kHalfBytes, m, 64 * c, head, row, bar);
             };
             tile(&mq, sb, h, sq.q0 + r0, qfull);
-            int issued = 0;
-            for (; issued < 2 * nt && !*abort_flag; ++issued) {
-                const int s = issued % NST;
-                if (issued >= NST && !mbar_wait(empty0 + 8 * s, ((issued / NST) - 1) & 1)) {
+            int nk = 0, nv = 0;  // tiles of K and of V requested
+            for (int j = 0; j < nt && ok && !*abort_flag; ++j) {
+                if (j >= NK && !mbar_wait(kempty + 8 * (j % NK), (j / NK - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                tile(issued & 1 ? &mv : &mk, sb + S::RING + s * TILE, hk, sq.k0 + (issued >> 1) * AT, full0 + 8 * s);
-                if (issued == 0) tile(&mdo, sb + TILE, h, sq.q0 + r0, dofull);
+                tile(&mk, sb + S::K + (j % NK) * TILE, hk, sq.k0 + j * AT, kfull + 8 * (j % NK));
+                ++nk;
+                if (j == 0) tile(&mdo, sb + TILE, h, sq.q0 + r0, dofull);
+                if (j >= NV && !mbar_wait(vempty + 8 * (j % NV), (j / NV - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tile(&mv, sb + S::V + (j % NV) * TILE, hk, sq.k0 + j * AT, vfull + 8 * (j % NV));
+                ++nv;
             }
             if (!ok) fail(ERR_PIPE_EMPTY_WAIT);
             if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
                 mbar_wait(qfull, 0);
-                if (issued) mbar_wait(dofull, 0);
-                for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full0 + 8 * (i % NST), (i / NST) & 1);
+                if (nk) mbar_wait(dofull, 0);
+                for (int j = max(0, nk - NK); j < nk; ++j) mbar_wait(kfull + 8 * (j % NK), (j / NK) & 1);
+                for (int j = max(0, nv - NV); j < nv; ++j) mbar_wait(vfull + 8 * (j % NV), (j / NV) & 1);
             }
-        } else if (warp == kAttnBwdMma && nt > 0) {
-            // ---------------- MMAs ----------------
+        } else if (warp < kAttnBwdLoad && nt > 0) {
+            // ---------------- MMAs: S and dP by one warp, dQ by the other ----------------
             constexpr uint32_t id_s = idesc_bf16(128, AT, false, false), id_d = idesc_bf16(128, D, false, true);
             const TileDesc desc(sb);
             const int tail = sq.lk - (nt - 1) * AT;  // rows of the last key tile, if fewer than 128
@@ -584,38 +633,48 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            // ring positions: K_j at 2 j, V_j at 2 j + 1
-            auto place = [](int pos) { return S::RING + (pos % NST) * TILE; };
-            // D[128 queries][128 keys] = (Q or dO) (K or V)^T, once the tile is there and what follows the sequence
-            // taken out
-            auto product = [&](uint32_t d, int rows, int pos, uint32_t commit) {
-                if (!wait(full0 + 8 * (pos % NST), (pos / NST) & 1)) return;
-                if (tail < AT && (pos >> 1) == nt - 1) zero_tail_rows<D>(sb + place(pos), tail, lane);
+            if (warp == kAttnBwdMma) {
+                // D[128 queries][128 keys] = (Q or dO) (K or V)^T, once the tile is there and what follows the sequence
+                // taken out
+                auto product = [&](uint32_t d, int rows, uint32_t full, uint32_t parity, int at, int j, uint32_t commit) {
+                    if (!wait(full, parity)) return;
+                    if (tail < AT && j == nt - 1) zero_tail_rows<D>(sb + at, tail, lane);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_ss_warp(d, desc.k(rows, ks), desc.k(place(pos), ks), id_s, ks > 0);
-                tc_commit_warp(commit);
-            };
-            auto score = [&](int j) { product(tmem + TM_S + 128 * (j & 1), 0, 2 * j, sfull0 + 8 * (j & 1)); };
-            auto dprob = [&](int j) {
-                product(tmem + TM_DP, TILE, 2 * j + 1, dpfull);
-                if (ok) tc_commit_warp(empty0 + 8 * ((2 * j + 1) % NST));
-            };
-            if (wait(qfull, 0)) score(0);
-            if (wait(dofull, 0)) dprob(0);
-            if (ok && nt > 1) score(1);
-            for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
-                const uint32_t a = tmem + TM_S + 128 * (j & 1);
-                if (j + 1 < nt && wait(dpfree, j & 1)) dprob(j + 1);
-                // (two barriers: dP of the next tile is on its way, so the warps may be done with that one's dS before
-                // this one's arrival is seen; the one after next waits for S, which is issued below)
-                if (!ok || !wait(dsready0 + 8 * (j & 1), (j >> 1) & 1)) break;
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc_mma_ss_warp(d, desc.k(rows, ks), desc.k(at, ks), id_s, ks > 0);
+                    tc_commit_warp(commit);
+                };
+                auto score = [&](int j) {
+                    const int st = j % NK;
+                    product(tmem + TM_S + 128 * (j & 1), 0, kfull + 8 * st, (j / NK) & 1, S::K + st * TILE, j,
+                            sfull0 + 8 * (j & 1));
+                };
+                auto dprob = [&](int j) {
+                    const int st = j % NV;
+                    product(tmem + TM_DP, TILE, vfull + 8 * st, (j / NV) & 1, S::V + st * TILE, j, dpfull);
+                    if (ok) tc_commit_warp(vempty + 8 * st);
+                };
+                if (wait(qfull, 0)) score(0);
+                if (wait(dofull, 0)) dprob(0);
+                if (ok && nt > 1) score(1);
+                for (int j = 0; j + 1 < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+                    if (wait(dpfree, j & 1)) dprob(j + 1);
+                    // dQ is done with dS of this tile, where S of the next but one goes
+                    if (j + 2 < nt && wait(kempty + 8 * (j % NK), (j / NK) & 1)) score(j + 2);
+                }
+            } else {
+                for (int j = 0; j < nt && ok && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+                    const int st = j % NK;
+                    const uint32_t a = tmem + TM_S + 128 * (j & 1);
+                    // (two barriers for dS: dP of the next tile is on its way, so the warps may be done with that one's
+                    // dS before this one's arrival is seen; the one after next waits for S, which waits for dQ)
+                    if (!wait(kfull + 8 * st, (j / NK) & 1) || !wait(dsready0 + 8 * (j & 1), (j >> 1) & 1)) break;
 #pragma unroll
-                for (int ks = 0; ks < AT / 16; ++ks)
-                    tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 1) * 32 + (ks & 1) * 8, desc.mn(place(2 * j), ks), id_d,
-                                   j > 0 || ks > 0);
-                tc_commit_warp(empty0 + 8 * ((2 * j) % NST));
-                if (j + 2 < nt) score(j + 2);
+                    for (int ks = 0; ks < AT / 16; ++ks)
+                        tc_mma_ts_warp(tmem + TM_DQ, a + (ks >> 1) * 32 + (ks & 1) * 8, desc.mn(S::K + st * TILE, ks),
+                                       id_d, j > 0 || ks > 0);
+                    tc_commit_warp(kempty + 8 * st);
+                }
             }
             tc_commit_warp(done);
             if (!ok && lane == 0) fail(ERR_PIPE_FULL_WAIT);
