@@ -279,7 +279,14 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
                     return ok;
                 };
                 // ring positions: K_j at 2 j, V_j at 2 j + 1
-                auto arrived = [&](int pos) { return wait(full0 + 8 * (pos % NST), (pos / NST) & 1); };
+                // (one issuer asks for each once, not for A, for B and to let it go: 229 -> 222 us, 8,192 tokens 16/4
+                // heads)
+                int seen[2] = {-1, -1};
+                auto arrived = [&](int pos) {
+                    if (!kOwnP && pos <= seen[pos & 1]) return ok;
+                    seen[pos & 1] = pos;
+                    return wait(full0 + 8 * (pos % NST), (pos / NST) & 1);
+                };
                 // An issuer lets go of every position, also of those that its tile does not use, but of none before it
                 // is there: an arrival ahead of the loads would count for the position's predecessor in the ring.
                 auto release = [&](int pos) {
