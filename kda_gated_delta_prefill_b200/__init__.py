@@ -480,16 +480,24 @@ def forward_noalloc(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, o=
 # ---------------------------------------------------------------------------------------------- softmax attention
 # These calls take a few microseconds on the GPU for short requests, so their host side is kept as short: pointers
 # as plain integers, the device switched only where it is not the current one.
-def _call(name, dev, stream, *args):
-    """Call a C entry whose last argument is the stream, on the tensors' device."""
+def _call(name, dev, *args):
+    """Call a C entry whose last argument is the stream, on the tensors' device and its current stream."""
     import torch
     if torch.cuda.current_device() != dev.index:
         with _on(dev):
-            return _call(name, dev, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    rc = getattr(_lib or lib(), name)(*args, s)
+            return _call(name, dev, *args)
+    rc = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != 0:
         raise KdaError(rc, name)
+
+
+def _under(stream, device):
+    """Makes ``stream`` the current one for a call, so that the workspace and the results it allocates are that stream's:
+    memory of another stream may still be in use there, or be given away again before this one is done with it."""
+    import torch
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _scale(scale, D):
@@ -554,6 +562,9 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
     scale: D^-0.5 when not given.  lse is the natural logarithm of the row's sum of exponentials.
     """
     import torch
+    if stream is not None:
+        with _under(stream, q.device):
+            return attention_forward(q, k, v, cu_seqlens, cu_seqlens_k, scale=scale, o=o, lse=lse)
     rows, dims, dev = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
     B, T, H, D = q.shape
     if o is None:
@@ -564,7 +575,7 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
         lse = torch.empty(B, H, T, dtype=torch.float32, device=dev)
     else:
         _need("lse", lse, torch.float32, B * H * T, dev)
-    _call("kda_attention_forward", dev, stream, *rows, *dims, _scale(scale, D), o.data_ptr(),
+    _call("kda_attention_forward", dev, *rows, *dims, _scale(scale, D), o.data_ptr(),
           lse.data_ptr())
     return o, lse
 
@@ -581,6 +592,9 @@ def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None
     key/value head.  dout's rows may be strided like q's.  Rows of no sequence are not written.
     """
     import torch
+    if stream is not None:
+        with _under(stream, q.device):
+            return attention_backward(q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_k, scale=scale, workspace=workspace)
     if q.dim() != 4 or dout.shape != q.shape:
         raise ValueError("q must be [B,T,H,D], dout like it, k and v [B,Tk,HKV,D]")
     B, T, H, D = q.shape
@@ -593,7 +607,7 @@ def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None
     dv = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     if workspace is None:
         workspace = torch.empty(attention_backward_workspace_size(B, T, H, dims[2]), dtype=torch.uint8, device=dev)
-    _call("kda_attention_backward", dev, stream, *rows, o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+    _call("kda_attention_backward", dev, *rows, o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
           _row_stride("dout", dout.shape, dout.stride()), *dims, _scale(scale, D), dq.data_ptr(),
           dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
@@ -616,6 +630,9 @@ def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num
     not fit gets -1 and sets bit 5 of ``device_error``.
     """
     import torch
+    if stream is not None:
+        with _under(stream, context_lens.device):
+            return cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num_tokens)
     B = context_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, width]")
@@ -631,7 +648,7 @@ def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num
     slots, cu, lens, used = torch.unsafe_split_with_sizes(buf, (num_tokens, B + 1, B, 1))
     at = buf.data_ptr()
     small = at + 4 * num_tokens
-    _call("kda_cache_plan", dev, stream, context_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
+    _call("kda_cache_plan", dev, context_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
           table_stride, width, free_blocks.data_ptr(), free_blocks.numel(), block_size, small,
           small + 4 * (B + 1), at, num_tokens, small + 4 * (2 * B + 1))
     return cu, lens, slots, used
@@ -674,6 +691,9 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map, *, stream=N
     need it.
     """
     import torch
+    if stream is not None:
+        with _under(stream, k.device):
+            return cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map)
     shape = k.shape
     if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be [T,HKV,D]")
@@ -685,7 +705,7 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map, *, stream=N
          ("slot_map", slot_map, torch.int32, T, True)))
     if hkv != HKV or d != D:
         raise ValueError("k and v must have the cache's heads")
-    _call("kda_cache_append", dev, stream, k.data_ptr(), _row_stride("k", shape, k.stride()), v.data_ptr(),
+    _call("kda_cache_append", dev, k.data_ptr(), _row_stride("k", shape, k.stride()), v.data_ptr(),
           _row_stride("v", shape, v.stride()), k_cache.data_ptr(), v_cache.data_ptr(), stride, k_scale.data_ptr(),
           v_scale.data_ptr(), code, blocks, bs, slot_map.data_ptr(), T, HKV, D)
 
@@ -704,6 +724,10 @@ def attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     lse = -inf).  scale: D^-0.5 when not given.  Blocks out of range do not count and set bit 4 of ``device_error``.
     """
     import torch
+    if stream is not None:
+        with _under(stream, q.device):
+            return attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale=scale, o=o, lse=lse,
+                                    workspace=workspace)
     qs, ts = q.shape, block_table.shape
     if len(qs) != 3 or len(ts) != 2 or ts[0] != qs[0]:
         raise ValueError("q must be [B,H,D] and block_table [B,width]")
@@ -730,7 +754,7 @@ def attention_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
                                 device=dev)
     else:
         _need("workspace", workspace, torch.uint8, None, dev)
-    _call("kda_attention_decode", dev, stream, q.data_ptr(), _row_stride("q", qs, q.stride()), k_cache.data_ptr(),
+    _call("kda_attention_decode", dev, q.data_ptr(), _row_stride("q", qs, q.stride()), k_cache.data_ptr(),
           v_cache.data_ptr(), stride, k_scale.data_ptr(), v_scale.data_ptr(), code, blocks, bs, block_table.data_ptr(),
           table_stride, width, seq_lens.data_ptr(), B, H, HKV, D, _scale(scale, D), o.data_ptr(),
           lse.data_ptr(), workspace.data_ptr(), workspace.numel())

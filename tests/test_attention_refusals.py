@@ -245,3 +245,18 @@ def test_binding_refuses_caches():
                       ((lens, lens, table, slots, 16, 9), "must be a CUDA tensor")]:
         with pytest.raises(ValueError, match=msg):
             kda.cache_plan(*args)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda s: kda.attention_forward(q, q, q, stream=s),
+                 lambda s: kda.attention_backward(q, q, q, q, q, q, stream=s),
+                 lambda s: kda.cache_plan(n, n, n[:, None], n, 16, 4, stream=s),
+                 lambda s: kda.cache_append(q[0], q[0], q, q, n, n, n, stream=s),
+                 lambda s: kda.attention_decode(q[0], q, q, n, n, n[:, None], n, stream=s)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call(Stream())

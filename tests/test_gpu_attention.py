@@ -261,6 +261,24 @@ def test_same_bits_on_every_run_and_stream():
         assert all(torch.equal(a, b) for a, b in zip(g, want))
 
 
+def test_a_stream_s_results_are_in_memory_of_that_stream():
+    """What a call on another stream allocates must not be memory that the current stream has yet to write to: work is
+    pending there on tensors that are already given back, of the sizes of the call's results and workspace."""
+    q, k, v, dout = heads(1, 1, 1024, 4, 64), heads(2, 1, 1024, 4, 64), heads(3, 1, 1024, 4, 64), heads(4, 1, 1024, 4, 64)
+    want = run(q, k, v, dout)
+    ws = torch.empty(kda.attention_backward_workspace_size(1, 1024, 4), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    late = [torch.empty_like(x).fill_(6) for x in (*want, ws)]  # (loads the kernels: that would wait for the pending work)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for x in late:
+        x.fill_(7)
+    del late, x
+    got = run(q, k, v, dout, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("T,H,HKV,D", [(4096, 32, 4, 128), (700, 16, 2, 128), (2100, 16, 4, 64)])
 def test_same_bits_over_many_runs(T, H, HKV, D):
     """The warps of a CTA meet at barriers whose phases must not run ahead of a slow one: hundreds of launches of thousands
