@@ -12,6 +12,10 @@ contract"): q, k [B,T,H,128] bf16; v [B,T,HV,128] bf16; g [B,T,HV,128]
 fp32; beta [B,T,HV] fp32; initial_state [N,HV,128,128] fp32 or None;
 cu_seqlens [N+1] int32 or None (then B must be 1).  Returns o
 [B,T,HV,128] bf16 and final_state [N,HV,128,128] fp32.
+
+Softmax attention for the full-attention layers beside it: ``attention_forward`` and
+``attention_backward`` over packed prompts, ``cache_plan``, ``cache_append`` and
+``attention_decode`` over a paged 8-bit key/value cache.
 """
 from __future__ import annotations
 

@@ -391,7 +391,7 @@ extern "C" kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, co
     p.err = info.err;
     // Windows as small as leaves 32 CTAs for each SM at most (3 fit at a time): one token for a step of requests, a
     // block for prompts.  256 single tokens (8 heads, blocks of 64): 6 us with one warp a unit, 14 with four; prompts
-    // of 97,000 tokens (blocks of 16, where both are the same) do not differ.
+    // of 95,000 tokens (blocks of 16, where both are the same) do not differ.
     const int wpu = block_size / 16;
     const int64_t wide = (2ll * HKV * wpu + 7) / 8;  // CTAs of a run with BS / 16 warps a unit
     const int64_t fits = T * wide / (32ll * info.sms);

@@ -32,8 +32,8 @@ namespace kda {
 
 // A tile is 16 KB of codes: 64 tokens at D = 128, 128 at D = 64, where a warp takes two slices of 16 tokens at once.
 // The warps' work on a tile is a chain of latencies (shared memory, MMAs, shuffles, exponentials, MMAs), so three CTAs
-// share an SM where registers allow it (up to 8 query heads): 161 -> 147 us for 512 int8 requests of up to 4,096
-// tokens.
+// share an SM where registers allow it (up to 8 query heads): 161 -> 147 us for 64 int8 requests of 500 to
+// 12,000 tokens, 32/8 heads.
 __host__ __device__ constexpr int ad_tile(int D) { return 64 * (128 / D); }
 __host__ __device__ constexpr int ad_ctas(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
