@@ -442,7 +442,7 @@ extern "C" size_t kda_attention_decode_workspace_size(int B, int H, int HKV, int
         block_shift(block_size) < 0)
         return 0;
     const int64_t ctas = decode_ctas(B, H, HKV, D, table_width, block_size);
-    return decode_part_bytes(ctas, H, HKV, D) + round_up(static_cast<size_t>(ctas) * sizeof(int2), kAlign);
+    return decode_part_bytes(ctas, H, HKV, D) + round_up(static_cast<size_t>(ctas) * 2 * sizeof(int4), kAlign);
 }
 
 extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride, const void *k_cache,
@@ -492,7 +492,7 @@ extern "C" kda_status_t kda_attention_decode(const void *q, int64_t q_row_stride
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
     p.part = static_cast<float *>(workspace);
-    p.shared_unit = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + decode_part_bytes(ctas, H, HKV, D));
+    p.shared_unit = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + decode_part_bytes(ctas, H, HKV, D));
     p.err = info.err;
     p.B = B;
     p.H = H;

@@ -41,6 +41,8 @@ constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
 // D = 128; us on the device with a cluster and without: 500 tokens 5.4, 8.5; 2,000: 7.1, 10.2; 8,000: 13, 15; 32,000:
 // 37, 21).
 constexpr int kAdCluster = 8, kAdClusterTiles = 128;
+// The join's threads, and the pieces times float4s of a unit that it joins in one CTA: eight for each thread.
+constexpr int kAdJoinThreads = 512, kAdJoinItems = 8 * kAdJoinThreads;
 
 struct AttnDecodeParams {
     const __nv_bfloat16 *q;  // row b at q + b * q_stride: [H, D]
@@ -52,7 +54,8 @@ struct AttnDecodeParams {
     __nv_bfloat16 *o;              // [B, H, D]
     float *lse;                    // [B, H]
     float *part;                   // [G][2] pieces: accumulators [HB][D], then reference and sum [HB][2]
-    int2 *shared_unit;             // [G]: the unit that begins in CTA c and goes on behind it (or -1), CTAs behind
+    int4 *shared_unit;             // [G][2]: the unit that begins in CTA c and goes on behind it, and the one that comes in
+                                   // from before (or -1); each with the CTAs behind its first, and that CTA
     unsigned *err;
     int B, H, HKV, chunks, width, num_blocks;  // chunks of HB query heads of a group
     float scale_log2;
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
             start[0] = row;
             *reinterpret_cast<int64_t *>(start + 2) = g0 - at * units_row;
         }
-        if (tid == 0) p.shared_unit[c] = make_int2(-1, 0);
+        if (tid < 2) p.shared_unit[2 * c + tid] = make_int4(-1, 0, 0, 0);
         __syncthreads();
         if (g0 >= g1) return;
         b = start[0];
@@ -290,6 +293,20 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                     }
                 }
                 id = far;
+            }
+            // A unit of several CTAs: from the one with its first tile to the one with its last.  (The CTAs behind the
+            // first only where the join may want their help; at most n G / W + 2 CTAs have a piece.)
+            if (!CL && lane == 0 && t1 - t0 < n &&
+                (t0 == 0 || (static_cast<int64_t>(n) * G + 2 * W) * (HB * D / 4) >= 2 * kAdJoinItems * W)) {
+                auto owner = [&](int64_t tile) {  // k with share(k) <= tile < share(k + 1)
+                    int k = static_cast<int>(tile * G / W);
+                    while (share(W, k + 1, G) <= tile) ++k;
+                    while (share(W, k, G) > tile) --k;
+                    return k;
+                };
+                const int64_t begin = g1 - left - t0;
+                const int k0 = t0 == 0 ? c : owner(begin), k1 = t1 == n ? c : owner(begin + n - 1);
+                p.shared_unit[2 * c + (t0 > 0)] = make_int4(b * units_row + u, k1 - k0, k0, 0);
             }
             next(t1);
         }
@@ -563,13 +580,6 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                     if (d == 0) *reinterpret_cast<float2 *>(part + HB * D + 2 * hd) = make_float2(M, l);
                 }
             }
-            if (!CL && t0 == 0 && t1 < n && tid == 0) {  // it goes on in the CTAs behind
-                const int64_t end = g1 + (n - t1) - 1;  // its last tile: in the CTA k with share(k) <= end < share(k + 1)
-                int k = static_cast<int>(end * G / W);
-                while (share(W, k + 1, G) <= end) ++k;
-                while (share(W, k, G) > end) --k;
-                p.shared_unit[c] = make_int2(b * units_row + u, k - c);
-            }
             next(t1);
         }
         if (CL && idle) {  // fewer tiles than CTAs: an empty piece
@@ -613,7 +623,6 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
 // Joins the pieces of a unit that began in CTA c, in their order.  A thread takes a head, four dims and a run of the
 // pieces; the runs are joined through shared memory.  Bound by the latency of its dependent loads (which unit;
 // references and accumulators, eight pieces at a time).
-constexpr int kAdJoinThreads = 512;
 struct AttnPiece {
     float M, l;
     float4 a;
@@ -637,46 +646,56 @@ __global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(co
     constexpr int HB = 8 * NT, PIECE = HB * (D + 2);
     __shared__ AttnPiece runs[kAdJoinThreads];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int c = blockIdx.x, tid = threadIdx.x;
-    const int2 su = p.shared_unit[c];
-    if (su.x < 0) return;
-    const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
-    const int b = su.x / units_row, u = su.x % units_row, hk = u / p.chunks, hc = u % p.chunks;
-    const int heads = min(HB, group - hc * HB), items = heads * (D / 4), nr = kAdJoinThreads / items;  // runs
-    const int item = tid % items, run = tid / items, hd = item / (D / 4), d = 4 * (item % (D / 4));
-    const int n = su.y + 1, k_begin = n * run / nr, k_end = run < nr ? n * (run + 1) / nr : 0;
-    // the piece of CTA c is its last one, those of the CTAs behind their first
-    const float *first = p.part + (2ll * c + 1) * PIECE, *rest = p.part + 2ll * c * PIECE;
-    AttnPiece all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int k0 = k_begin; k0 < k_end; k0 += 8) {
-        float2 ml[8];
-        float4 v[8];
-        float M = all.M;
+    const int tid = threadIdx.x, units_row = p.HKV * p.chunks, group = p.H / p.HKV;
+    // A share of a unit's heads: all of them, unless there are so many pieces that a run would be longer than eight;
+    // then the CTAs behind the first take shares too (one request of 131,072 tokens, 8/1 heads: 44 -> 20 us for the
+    // step).
+    auto join = [&](int4 su, int part) {
+        const int c = su.z, b = su.x / units_row, u = su.x % units_row, hk = u / p.chunks, hc = u % p.chunks;
+        const int heads = min(HB, group - hc * HB), n = su.y + 1;
+        const int parts = max(1, min(heads, n * heads * (D / 4) / kAdJoinItems));
+        if (part >= parts) return;
+        const int h0 = heads * part / parts, items = (heads * (part + 1) / parts - h0) * (D / 4);
+        const int nr = kAdJoinThreads / items;  // runs
+        const int item = tid % items, run = tid / items, hd = h0 + item / (D / 4), d = 4 * (item % (D / 4));
+        const int k_begin = n * run / nr, k_end = run < nr ? n * (run + 1) / nr : 0;
+        // the piece of CTA c is its last one, those of the CTAs behind their first
+        const float *first = p.part + (2ll * c + 1) * PIECE, *rest = p.part + 2ll * c * PIECE;
+        AttnPiece all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int k0 = k_begin; k0 < k_end; k0 += 8) {
+            float2 ml[8];
+            float4 v[8];
+            float M = all.M;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + k < k_end) {
-                const float *src = k0 + k == 0 ? first : rest + 2ll * (k0 + k) * PIECE;
-                ml[k] = *reinterpret_cast<const float2 *>(src + HB * D + 2 * hd);
-                v[k] = *reinterpret_cast<const float4 *>(src + hd * D + d);
+            for (int k = 0; k < 8; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < k_end) {
+                    const float *src = k0 + k == 0 ? first : rest + 2ll * (k0 + k) * PIECE;
+                    ml[k] = *reinterpret_cast<const float2 *>(src + HB * D + 2 * hd);
+                    v[k] = *reinterpret_cast<const float4 *>(src + hd * D + d);
+                }
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) M = fmaxf(M, ml[k].x);
+            all.refer(M);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) all.add(ml[k].x, ml[k].y, v[k]);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) M = fmaxf(M, ml[k].x);
-        all.refer(M);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) all.add(ml[k].x, ml[k].y, v[k]);
-    }
-    runs[tid] = all;
-    __syncthreads();
-    if (run > 0) return;
-    for (int r = 1; r < nr; ++r) {
-        const AttnPiece &o = runs[r * items + item];
-        all.refer(fmaxf(all.M, o.M));
-        all.add(o.M, o.l, o.a);
-    }
-    store_attention<D>(p, b, hk * group + hc * HB + hd, d, all.a, all.M, all.l);
+        __syncthreads();  // (the runs of the share before are read)
+        runs[tid] = all;
+        __syncthreads();
+        if (run > 0) return;
+        for (int r = 1; r < nr; ++r) {
+            const AttnPiece &o = runs[r * items + item];
+            all.refer(fmaxf(all.M, o.M));
+            all.add(o.M, o.l, o.a);
+        }
+        store_attention<D>(p, b, hk * group + hc * HB + hd, d, all.a, all.M, all.l);
+    };
+    const int4 out = p.shared_unit[2 * blockIdx.x], in = p.shared_unit[2 * blockIdx.x + 1];
+    if (out.x >= 0) join(out, 0);
+    if (in.x >= 0) join(in, blockIdx.x - in.z);
 }
 
 }  // namespace kda

@@ -339,6 +339,25 @@ def test_decode_matches_the_formula(dtype, lens, H, HKV, D, bs):
     check_decode(args, lens, o, lse)
 
 
+@pytest.mark.parametrize("lens,H,HKV,D,bs", [
+    ([30000], 8, 1, 128, 64),        # one unit over every CTA: its heads are joined by as many CTAs as it has heads
+    ([30001], 1, 1, 64, 128),        # ... one head
+    ([28300], 5, 1, 128, 16),
+    ([27000], 16, 1, 64, 32),
+    ([27000], 12, 1, 128, 128),
+    ([9000, 3, 21000], 14, 2, 128, 64),
+    ([0, 14000, 14000, 1], 6, 3, 64, 64),
+])
+def test_decode_of_few_long_units(lens, H, HKV, D, bs):
+    args = make_decode(E4M3, lens, H, HKV, D, bs, 77)
+    got = kda.attention_decode(*args, i32(lens))
+    torch.cuda.synchronize()
+    assert kda.device_error() == 0
+    check_decode(args, lens, *got)
+    again = kda.attention_decode(*args, i32(lens))
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
 def test_decode_rows_of_packed_qkv_scale_and_given_buffers():
     lens, H, HKV, D = [300, 17, 0, 64], 8, 2, 128
     args = make_decode(E4M3, lens, H, HKV, D, 64, 3)
