@@ -200,6 +200,12 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     p.kslots = block_slots<AT>(d.N, Tk, d.packed);
     p.scale = scale;
     p.scale_log2 = scale * kLog2e;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_row_stride;
+    p.k_stride = k_row_stride;
+    p.v_stride = v_row_stride;
     p.o = static_cast<const __nv_bfloat16 *>(o);
     p.dout = static_cast<const __nv_bfloat16 *>(dout);
     p.do_stride = dout_row_stride;
@@ -248,7 +254,9 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     auto run = [&](auto stats, auto dkv, int dkv_smem, auto dqk, int dq_smem) {
         kda_status_t r = KDA_OK;
         if (d.rows) {
-            stats<<<p.qslots * H, kAttnStatThreads, 0, s>>>(p);
+            const int64_t grid = (static_cast<int64_t>(p.qslots) + d.N) * H;
+            if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
+            stats<<<static_cast<int>(grid), kAttnStatThreads, 0, s>>>(p);
             if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
         }
         if (d.krows) r = launch(dkv, static_cast<int64_t>(p.kslots) * HKV * p.split, dkv_smem, p.split, d.rows > 0);

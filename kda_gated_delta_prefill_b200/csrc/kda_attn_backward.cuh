@@ -12,10 +12,11 @@
 // instead of 5).
 //
 // Precision.  P and dS are rounded to bf16 for the products (2^-9 relative), and delta inherits the rounding of o:
-// where one key has most of a row's probability, dP_ij - delta_i is a small difference of it.  dQ and dK are 2.5e-3 off
-// for scores of unit variance and up to 5e-3 where the softmax is all but one-hot (of the 2-norm; 1.7e-3 is bf16
-// results alone). delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then
-// has to follow dQ, and a backward took 15-40 % longer.
+// where one key has most of a row's probability, dP_ij - delta_i is a small difference of it.  Rows that see at most 16
+// keys get delta in fp32 from its definition instead (statistics, below).  dQ and dK are 2.5e-3 off for scores of unit
+// variance and up to 5e-3 where the softmax over many keys is all but one-hot (of the 2-norm; 1.7e-3 is bf16 results
+// alone).  Delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then has to
+// follow dQ, and a backward took 15-40 % longer.
 //
 // dK/dV works on the transposes: a thread owns a key row of S^T = K Q^T and dP^T = V dO^T, so P^T and dS^T go back to
 // TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
@@ -41,8 +42,8 @@ struct AttnBwdParams {
     int H, HKV, qslots, kslots;  // slots of 128 rows of q and of k
     int split;                   // CTAs (a cluster) that share a key tile's query heads
     float scale, scale_log2;
-    const __nv_bfloat16 *o, *dout;
-    int64_t do_stride;
+    const __nv_bfloat16 *q, *k, *v, *o, *dout;
+    int64_t q_stride, k_stride, v_stride, do_stride;
     const float *lse;
     float *stats;  // [H][qslots][2][128]: -lse * log2(e) (-inf: no probability), -delta
     __nv_bfloat16 *dq, *dk, *dv;
@@ -50,43 +51,89 @@ struct AttnBwdParams {
 };
 
 // ---------------------------------------------------------------------------------------------------- statistics
-// A warp per row: bound by reading o and dout once.
-constexpr int kAttnStatThreads = 256;
+// A warp for two or four rows: bound by reading o and dout once.
+//
+// Rows that see few keys get delta from its definition, sum_j P_ij dP_ij in fp32: there P is large and dP_ij - delta_i
+// a small difference of two numbers, for which o . do with its rounded o is too coarse (sequences of two tokens: dQ
+// 2.7e-2 off, 2.5e-3 so).  They are the first 16 of a sequence's rows that see any; CTAs of their own take them, a
+// thread for each row and key (in the tiles' CTAs, behind the other rows, they cost 4 us of a 52 us backward).
+constexpr int kAttnStatThreads = 256, kAttnExactKeys = 16;
+// Eight products of bf16 values, summed.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b)
+{
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += bf16lo(x[e]) * bf16lo(y[e]) + bf16hi(x[e]) * bf16hi(y[e]);
+    return s;
+}
+// -lse * log2(e) of a row; -inf where it has no probability.
+__device__ __forceinline__ float neg_lse(const AttnBwdParams &p, int n, int h, const Seq &sq, int row)
+{
+    const int64_t at = p.seq.cu_q ? static_cast<int64_t>(h) * p.seq.T + sq.q0 + row
+                                  : (static_cast<int64_t>(n) * p.H + h) * p.seq.T + row;
+    return p.lse[at] == -INFINITY ? -INFINITY : -p.lse[at] * kLog2e;
+}
 template <int D>
-__global__ void __launch_bounds__(kAttnStatThreads) kda_attn_stats_kernel(const AttnBwdParams p)
+__device__ __forceinline__ void attn_exact_delta(const AttnBwdParams &p, int n, int h)
+{
+    static_assert(kAttnStatThreads == kAttnExactKeys * kAttnExactKeys, "a thread for each row and key");
+    const Seq sq = seq_of(p.seq, n);
+    const int diff = sq.lk - sq.lq;  // row i sees i + 1 + diff keys
+    const int row = max(0, -diff) + threadIdx.x / kAttnExactKeys, key = threadIdx.x % kAttnExactKeys;
+    const bool mine = row < min(sq.lq, kAttnExactKeys - diff);
+    const int hk = h / (p.H / p.HKV);
+    float x = 0.f;
+    if (mine && key <= row + diff) {
+        const int64_t i = static_cast<int64_t>(sq.q0) + row, j = static_cast<int64_t>(sq.k0) + key;
+        const uint4 *q = reinterpret_cast<const uint4 *>(p.q + i * p.q_stride + h * D),
+                    *g = reinterpret_cast<const uint4 *>(p.dout + i * p.do_stride + h * D),
+                    *k = reinterpret_cast<const uint4 *>(p.k + j * p.k_stride + hk * D),
+                    *v = reinterpret_cast<const uint4 *>(p.v + j * p.v_stride + hk * D);
+        float s = 0.f, dp = 0.f;
+#pragma unroll 2
+        for (int d = 0; d < D / 8; ++d) {
+            s += dot8(q[d], k[d]);
+            dp += dot8(g[d], v[d]);
+        }
+        x = ex2(fmaf(s, p.scale_log2, neg_lse(p, n, h, sq, row))) * dp;
+    }
+#pragma unroll
+    for (int off = kAttnExactKeys / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + row / AT;
+    if (mine && key == 0) p.stats[(static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT) + AT + row % AT] = -x;
+}
+// CTAs: of each head, the sequences (rows that see few keys), then the tiles.
+template <int D>
+__global__ void __launch_bounds__(kAttnStatThreads, 8) kda_attn_stats_kernel(const AttnBwdParams p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H - p.seq.N;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (slot < 0) {
+        attn_exact_delta<D>(p, slot + p.seq.N, h);
+        return;
+    }
     int n, blk;
     if (!find_block<AT>(p.seq.cu_q, p.seq.N, p.seq.T, slot, lane, n, blk)) return;
     const Seq sq = seq_of(p.seq, n);
+    const int few = kAttnExactKeys - (sq.lk - sq.lq);  // rows before it that see a key are left to the others
     float *out = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
     constexpr int R = AT / (kAttnStatThreads / 32);
     constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp at a time
     for (int i = 0; i < R; i += RPW) {
         const int r = warp * R + i + lane / LPR, row = blk * AT + r;
         float s = 0.f;
-        if (row < sq.lq) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p.o + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D +
-                                                             8 * (lane % LPR));
-            const uint4 b = *reinterpret_cast<const uint4 *>(p.dout + (static_cast<int64_t>(sq.q0) + row) * p.do_stride +
-                                                             h * D + 8 * (lane % LPR));
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s += bf16lo(x[e]) * bf16lo(y[e]) + bf16hi(x[e]) * bf16hi(y[e]);
-        }
+        if (row < sq.lq)
+            s = dot8(*reinterpret_cast<const uint4 *>(p.o + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D +
+                                                      8 * (lane % LPR)),
+                     *reinterpret_cast<const uint4 *>(p.dout + (static_cast<int64_t>(sq.q0) + row) * p.do_stride +
+                                                      h * D + 8 * (lane % LPR)));
 #pragma unroll
         for (int off = LPR / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         if (lane % LPR == 0) {
-            float l2 = -INFINITY;
-            if (row < sq.lq) {
-                const int64_t at = p.seq.cu_q ? static_cast<int64_t>(h) * p.seq.T + sq.q0 + row
-                                              : (static_cast<int64_t>(n) * p.H + h) * p.seq.T + row;
-                l2 = p.lse[at] == -INFINITY ? -INFINITY : -p.lse[at] * kLog2e;
-            }
-            out[r] = l2;
-            out[AT + r] = -s;
+            out[r] = row < sq.lq ? neg_lse(p, n, h, sq, row) : -INFINITY;
+            if (row >= min(few, sq.lq) || row < sq.lq - sq.lk) out[AT + r] = -s;
         }
     }
 }

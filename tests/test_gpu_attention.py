@@ -245,6 +245,34 @@ def test_gradients_against_differences(D):
         assert (got - want).abs() <= tol and tol < 0.5 * (grads[i].double() * u).abs().sum()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,klens", [([1, 2, 3, 2, 16, 2, 5, 2, 2, 11, 2], None),
+                                        ([3, 20, 2, 140], [16, 10, 1, 5])])
+def test_gradients_of_rows_that_see_few_keys(D, lens, klens):
+    """There P (dP - delta) is a small difference of large numbers, and delta = o . dout with its rounded o too coarse.
+    The tolerance counts the roundings of P, dS and the results, and for dP and delta those of fp32 sums of D products alone:
+    D 2^-24 <= 2^-17 of the products' sizes, twice that for the tensor cores' additions, so 2^-8 half steps of bf16."""
+    klens = klens or lens
+    H, HKV, scale = 8, 2, D ** -0.5
+    q, dout = heads(11, 1, sum(lens), H, D, gain=1.0), heads(12, 1, sum(lens), H, D)
+    k, v = heads(13, 1, sum(klens), HKV, D, gain=1.0), heads(14, 1, sum(klens), HKV, D)
+    grads = run(q, k, v, dout, cu_of(lens), cu_of(klens))[2:]
+    for _, a, n, c, m in sequences(1, 0, 0, lens, klens):
+        x = [t[0, a:a + n].double().transpose(0, 1) for t in (q, dout)]
+        kk, vv = (t[0, c:c + m].double().repeat_interleave(H // HKV, 1).transpose(0, 1) for t in (k, v))
+        f = formula(q[0, a:a + n], k[0, c:c + m], v[0, c:c + m], scale, dout[0, a:a + n])
+        seen = torch.arange(m, device="cuda")[None] <= torch.arange(n, device="cuda")[:, None] + m - n
+        p = torch.exp((x[0] @ kk.transpose(1, 2) * scale) - f["lse"].nan_to_num(0, 0, 0)[..., None]) * seen
+        dp, dp_w = x[1] @ vv.transpose(1, 2), x[1].abs() @ vv.abs().transpose(1, 2)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True)) * scale
+        w = ds.abs() + p * scale * 2.0 ** -8 * (dp_w + (p * dp_w).sum(-1, keepdim=True))
+        dk_w = (w.transpose(1, 2) @ x[0].abs()).view(HKV, H // HKV, m, D).sum(1).transpose(0, 1)
+        for got, want, weight in ((grads[0][0, a:a + n], f["dq"], (w @ kk.abs()).transpose(0, 1)),
+                                  (grads[1][0, c:c + m], f["dk"], dk_w)):
+            tol = (HALF + FP32) * weight + HALF * want.abs() + 1e-30
+            assert ((got.double() - want).abs() <= tol).all(), (a, n, m)
+
+
 def test_same_bits_on_every_run_and_stream():
     q, k, v, dout = heads(1, 1, 2000, 8, 128), heads(2, 1, 2000, 2, 128), heads(3, 1, 2000, 2, 128), heads(4, 1, 2000, 8, 128)
     cu = cu_of([700, 1, 1299])
