@@ -103,7 +103,8 @@ __device__ __forceinline__ void attn_exact_delta(const AttnBwdParams &p, int n, 
     const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + row / AT;
     if (mine && key == 0) p.stats[(static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT) + AT + row % AT] = -x;
 }
-// CTAs: of each head, the sequences (rows that see few keys), then the tiles.
+// CTAs: of each head, the sequences (rows that see few keys), then the tiles.  32 registers, so that eight of them fit an
+// SM and keep enough loads in flight (40 registers: 33 us instead of 29 for 16,384 tokens and 16 heads).
 template <int D>
 __global__ void __launch_bounds__(kAttnStatThreads, 8) kda_attn_stats_kernel(const AttnBwdParams p)
 {
