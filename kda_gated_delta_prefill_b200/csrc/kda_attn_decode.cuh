@@ -20,10 +20,15 @@
 // of two makes its largest element 1..2 (exact, but for elements 2^-14 smaller than it, which round at 2^-24 of it).
 // tcgen05 would want the codes in shared memory as fp16, and at 24 bytes per cycle and SM mma.sync is not what bounds.
 //
-// The value scale goes into the exponent: with t_j = s_j log2(e) + log2(vs_b), the weights p_j = 2^(t_j - M) are
-// what multiplies the codes and p_j / vs_b is what the softmax's sum adds.  M is a running reference of t, so a weight
-// is small only where its product with the codes is.  Weights are fp16 (11 bits), 2^12 at the reference and at most
-// 2^15, which keeps what is flushed below 2^-37 of the largest.
+// The value scale goes into the exponent: with x_j = s_j log2(e) and t_j = x_j + log2(vs_b), the weights 2^(t_j - M) are
+// what multiplies the codes.  M is a running reference of t, so a weight is small only where its product with the codes
+// is.  Weights are fp16 (11 bits), 2^12 where M is set and at most 2^15, which keeps what is flushed below 2^-37 of the
+// largest.  The softmax's sum has a running reference of its own, L of x, and adds 2^(x_j - L).  (With one reference for
+// both, 1 / vs_b is a factor of the sum, which then overflows for small scales, such as 65,536 tokens of a cache of zeros
+// at scale 2^-100, and loses blocks whose scales are far below another's.)  The term is the weight times
+// 2^(M - L) / vs_b, one factor for 16 tokens of a block.  Where that factor passes 2^48 the weights, which fp16 flushes
+// anyway, are formed with the scale 2^(M - L - 48), so that they do not underflow before the sum has them.
+// What leaves a warp, a CTA or a piece is M, the accumulator, and log2 of the whole sum.
 #pragma once
 #include "kda_attn_common.cuh"
 #include "kda_cache.cuh"
@@ -53,7 +58,7 @@ struct AttnDecodeParams {
     const int32_t *lens;           // [B]
     __nv_bfloat16 *o;              // [B, H, D]
     float *lse;                    // [B, H]
-    float *part;                   // [G][2] pieces: accumulators [HB][D], then reference and sum [HB][2]
+    float *part;                   // [G][2] pieces: accumulators [HB][D], then reference and log2 of the sum [HB][2]
     int4 *shared_unit;             // [G][2]: the unit that begins in CTA c and goes on behind it, and the one that comes in
                                    // from before (or -1); each with the CTAs behind its first, and that CTA
     unsigned *err;
@@ -104,15 +109,32 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
     }
 }
 
-// Four dims of a head's result from its accumulator, reference and sum (0: no token counted).
+// log2 of a sum with its reference; -inf: no token counted.
+// (lg2.approx is off by 2^-22, of itself or, between 1/2 and 2, absolutely)
+__device__ __forceinline__ float log_sum(float L, float l)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(l));
+    return l == 0.f ? -INFINITY : L + y;
+}
+// What a piece's accumulator (its reference Mk at most M) and sum are multiplied by and add, when pieces are joined.
+__device__ __forceinline__ float join_weight(float Mk, float Lk, float M)
+{
+    return Mk == -INFINITY ? (Lk == -INFINITY ? 0.f : 1.f) : ex2_ftz(Mk - M);
+}
+__device__ __forceinline__ float join_sum(float Lk, float L) { return Lk == -INFINITY ? 0.f : ex2_ftz(Lk - L); }
+
+// Four dims of a head's result from its accumulator, reference and log2 of the sum.
 template <int D>
-__device__ __forceinline__ void store_attention(const AttnDecodeParams &p, int b, int h, int d, float4 a, float M, float l)
+__device__ __forceinline__ void store_attention(const AttnDecodeParams &p, int b, int h, int d, float4 a, float M, float L)
 {
     const int64_t at = static_cast<int64_t>(b) * p.H + h;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool none = L == -INFINITY;
+    const float f = ex2(0.5f * (M - L));  // in two steps: the whole may be below 2^-149
     *reinterpret_cast<uint2 *>(p.o + at * D + d) =
-        l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-    if (d == 0) p.lse[at] = l == 0.f ? -INFINITY : (M - 12.f + log2f(l)) * kLn2;
+        none ? make_uint2(0u, 0u)
+             : make_uint2(pack_bf16(a.x * f * f, a.y * f * f), pack_bf16(a.z * f * f, a.w * f * f));
+    if (d == 0) p.lse[at] = none ? -INFINITY : L * kLn2;
 }
 
 template <bool FP8, int D, int NT, bool CL>
@@ -264,10 +286,10 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                     vs = p.vscale[static_cast<int64_t>(id) * p.HKV + hk];
                 }
                 if (__any_sync(0xffffffffu, id == -1) && lane == 0) atomicOr(p.err, ERR_BLOCK_ID);
-                // a slice that counts: scale of the scores, log2 and inverse of the value scale.  All of a block's
-                // values are zero where its scale is: any scale will do then
-                const float v1 = vs > 0.f ? vs : 1.f;
-                const float4 m = make_float4(ks, log2f(v1), 1.f / v1, id >= 0 ? (vs > 0.f ? 1.f : 2.f) : 0.f);
+                // scale of the scores, log2 of the value scale and that + 48, whether the slice counts (1 or 2).  All
+                // of a block's values are zero where its scale is (2): any scale will do then
+                const float lv = log2f(vs > 0.f ? vs : 1.f);
+                const float4 m = make_float4(ks, lv, lv + 48.f, id >= 0 ? (vs > 0.f ? 1.f : 2.f) : 0.f);
                 const bool copies = id >= 0 && my_slice % slices_page == 0;  // the lane of a copy's first slice
                 const uint32_t who = __ballot_sync(0xffffffffu, copies);
                 for (int k = 0; k < BATCH && t + k < t1; ++k, ++it) {
@@ -364,11 +386,12 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                 f1[nt] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
             }
             if (ok && lane == 0) mbar_arrive(qempty0 + 8 * qs);
-            float acc[NT][MT][4], M0[NT], M1[NT], l0[NT], l1[NT];
+            float acc[NT][MT][4], l0[NT], l1[NT];
+            float M0[NT], M1[NT], Q0[NT], Q1[NT];  // M, M - L
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 M0[nt] = M1[nt] = -INFINITY;
-                l0[nt] = l1[nt] = 0.f;
+                Q0[nt] = Q1[nt] = l0[nt] = l1[nt] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
             }
@@ -427,7 +450,8 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                     uint32_t pb[SL][NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float h0 = -INFINITY, h1 = -INFINITY;
+                        float h0 = -INFINITY, h1 = -INFINITY;  // largest t
+                        bool low = false;
 #pragma unroll
                         for (int y = 0; y < SL; ++y) {
                             const float a = f0[nt] * m[y].x, bq = f1[nt] * m[y].x;
@@ -440,20 +464,39 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                             if (r + 8 >= have[y]) x[2] = x[3] = -INFINITY;
                             h0 = fmaxf(h0, fmaxf(x[0], x[2]));
                             h1 = fmaxf(h1, fmaxf(x[1], x[3]));
+                            low = low || m[y].z < Q0[nt] || m[y].z < Q1[nt];
                         }
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) {
                             h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, off));
                             h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, off));
                         }
-                        const bool g0_ = h0 > M0[nt] + 3.f, g1_ = h1 > M1[nt] + 3.f;
-                        if (__any_sync(0xffffffffu, g0_ || g1_)) {
-                            const float n0 = g0_ ? h0 : M0[nt], n1 = g1_ ? h1 : M1[nt];
-                            const float al0 = g0_ ? ex2(M0[nt] - n0) : 1.f, al1 = g1_ ? ex2(M1[nt] - n1) : 1.f;
-                            M0[nt] = n0;
-                            M1[nt] = n1;
-                            l0[nt] *= al0;
-                            l1[nt] *= al1;
+                        // L moves where M does: a term is at most its weight, 2^15, times 2^48 without
+                        const bool g0_ = h0 > M0[nt] + 15.f, g1_ = h1 > M1[nt] + 15.f;
+                        const bool moves = __any_sync(0xffffffffu, g0_ || g1_ || low) != 0;
+                        if (moves) {
+                            float x0 = -INFINITY, x1 = -INFINITY;  // largest x
+#pragma unroll
+                            for (int y = 0; y < SL; ++y) {
+                                x0 = fmaxf(x0, (SL == 1 ? h0 : fmaxf(s[y][nt][0], s[y][nt][2])) - m[y].y);
+                                x1 = fmaxf(x1, (SL == 1 ? h1 : fmaxf(s[y][nt][1], s[y][nt][3])) - m[y].y);
+                            }
+#pragma unroll
+                            for (int off = 4; SL > 1 && off < 32; off <<= 1) {
+                                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                            }
+                            // the accumulators' factor; the sum's reference M - Q goes from M - Q to Mn - Qn
+                            auto move = [](float &M, float &Q, float &l, bool g, float h, float x) {
+                                const float Mn = g ? h - 12.f : M, L = M - Q;
+                                const float Qn = g || x > L ? Mn - fmaxf(L, x) : Q, dm = g ? M - Mn : 0.f;
+                                l *= ex2_ftz(dm + (Qn - Q));
+                                M = Mn;
+                                Q = Qn;
+                                return ex2_ftz(dm);
+                            };
+                            const float al0 = move(M0[nt], Q0[nt], l0[nt], g0_, h0, x0);
+                            const float al1 = move(M1[nt], Q1[nt], l1[nt], g1_, h1, x1);
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
                                 acc[nt][i][0] *= al0;
@@ -462,17 +505,24 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                                 acc[nt][i][3] *= al1;
                             }
                         }
-                        const float e0 = 12.f - M0[nt], e1 = 12.f - M1[nt];
 #pragma unroll
                         for (int y = 0; y < SL; ++y) {
                             float(&x)[4] = s[y][nt];
-                            x[0] = ex2(x[0] + e0);
-                            x[1] = ex2(x[1] + e1);
-                            x[2] = ex2(x[2] + e0);
-                            x[3] = ex2(x[3] + e1);
+                            float e0 = -M0[nt], e1 = -M1[nt], c0 = Q0[nt] - m[y].y, c1 = Q1[nt] - m[y].y;
+                            if (moves) {  // factors of 2^48 at most
+                                const float u0 = fmaxf(c0 - 48.f, 0.f), u1 = fmaxf(c1 - 48.f, 0.f);
+                                e0 += u0;
+                                e1 += u1;
+                                c0 -= u0;
+                                c1 -= u1;
+                            }
+                            x[0] = ex2_ftz(x[0] + e0);
+                            x[1] = ex2_ftz(x[1] + e1);
+                            x[2] = ex2_ftz(x[2] + e0);
+                            x[3] = ex2_ftz(x[3] + e1);
                             if (SL > 1 && have[y] <= 0) x[0] = x[1] = x[2] = x[3] = 0.f;  // (before any token: M is -inf)
-                            l0[nt] = fmaf(x[0] + x[2], m[y].z, l0[nt]);
-                            l1[nt] = fmaf(x[1] + x[3], m[y].z, l1[nt]);
+                            l0[nt] = fmaf(x[0] + x[2], ex2_ftz(c0), l0[nt]);
+                            l1[nt] = fmaf(x[1] + x[3], ex2_ftz(c1), l1[nt]);
                             pb[y][nt][0] = movmatrix(pack_f16(x[0], x[1]));
                             pb[y][nt][1] = movmatrix(pack_f16(x[2], x[3]));
                         }
@@ -547,9 +597,9 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
                 if (r == 0) {
                     float *st = stats + (warp * HB + 8 * nt + 2 * cc) * 2;
                     st[0] = M0[nt];
-                    st[1] = l0[nt];
+                    st[1] = log_sum(M0[nt] - Q0[nt], l0[nt]);
                     st[2] = M1[nt];
-                    st[3] = l1[nt];
+                    st[3] = log_sum(M1[nt] - Q1[nt], l1[nt]);
                 }
             }
             asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAdWarps) : "memory");
@@ -557,27 +607,31 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
             float *part = p.part + static_cast<int64_t>(2 * c + (t0 > 0 ? 0 : 1)) * (HB * (D + 2));
             for (int i = tid; i < heads * (D / 4); i += 32 * kAdWarps) {
                 const int hd = i / (D / 4), d = 4 * (i % (D / 4));
-                float M = -INFINITY;
+                float M = -INFINITY, L = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kAdWarps; ++w) M = fmaxf(M, stats[(w * HB + hd) * 2]);
+                for (int w = 0; w < kAdWarps; ++w) {
+                    M = fmaxf(M, stats[(w * HB + hd) * 2]);
+                    L = fmaxf(L, stats[(w * HB + hd) * 2 + 1]);
+                }
                 float l = 0.f;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kAdWarps; ++w) {
-                    const float Mw = stats[(w * HB + hd) * 2], lw = stats[(w * HB + hd) * 2 + 1];
-                    const float f = Mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2(Mw - M);
+                    const float Mw = stats[(w * HB + hd) * 2], Lw = stats[(w * HB + hd) * 2 + 1];
+                    const float f = join_weight(Mw, Lw, M);
                     const float4 v = *reinterpret_cast<const float4 *>(join + (w * HB + hd) * D + d);
-                    l = fmaf(lw, f, l);
+                    l += join_sum(Lw, L);
                     a = make_float4(fmaf(v.x, f, a.x), fmaf(v.y, f, a.y), fmaf(v.z, f, a.z), fmaf(v.w, f, a.w));
                 }
+                L = log_sum(L, l);
                 if constexpr (CL) {  // this CTA's piece, in shared memory
                     reinterpret_cast<float4 *>(sm + S::QROWS)[i] = a;
-                    if (d == 0) reinterpret_cast<float2 *>(sm + S::META)[hd] = make_float2(M, l);
+                    if (d == 0) reinterpret_cast<float2 *>(sm + S::META)[hd] = make_float2(M, L);
                 } else if (whole) {
-                    store_attention<D>(p, b, head0 + hd, d, a, M, l);
+                    store_attention<D>(p, b, head0 + hd, d, a, M, L);
                 } else {
                     *reinterpret_cast<float4 *>(part + hd * D + d) = a;
-                    if (d == 0) *reinterpret_cast<float2 *>(part + HB * D + 2 * hd) = make_float2(M, l);
+                    if (d == 0) *reinterpret_cast<float2 *>(part + HB * D + 2 * hd) = make_float2(M, L);
                 }
             }
             next(t1);
@@ -585,7 +639,7 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
         if (CL && idle) {  // fewer tiles than CTAs: an empty piece
             for (int i = tid; i < HB * D / 4; i += 32 * kAdWarps)
                 reinterpret_cast<float4 *>(sm + S::QROWS)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (tid < HB) reinterpret_cast<float2 *>(sm + S::META)[tid] = make_float2(-INFINITY, 0.f);
+            if (tid < HB) reinterpret_cast<float2 *>(sm + S::META)[tid] = make_float2(-INFINITY, -INFINITY);
         }
     }
     if constexpr (CL) {
@@ -598,22 +652,25 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
             if (hd >= heads) continue;
             float2 ml[kAdCluster];
             float4 v[kAdCluster];
-            float M = -INFINITY, l = 0.f;
+            float M = -INFINITY, L = -INFINITY, l = 0.f;
 #pragma unroll
             for (int k = 0; k < kAdCluster; ++k) {
                 ml[k] = cluster_load2(sb + S::META + 8 * hd, k);
                 v[k] = cluster_load4(sb + S::QROWS + (hd * D + d) * 4, k);
             }
 #pragma unroll
-            for (int k = 0; k < kAdCluster; ++k) M = fmaxf(M, ml[k].x);
+            for (int k = 0; k < kAdCluster; ++k) {
+                M = fmaxf(M, ml[k].x);
+                L = fmaxf(L, ml[k].y);
+            }
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kAdCluster; ++k) {
-                const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - M);
-                l = fmaf(ml[k].y, f, l);
+                const float f = join_weight(ml[k].x, ml[k].y, M);
+                l += join_sum(ml[k].y, L);
                 a = make_float4(fmaf(v[k].x, f, a.x), fmaf(v[k].y, f, a.y), fmaf(v[k].z, f, a.z), fmaf(v[k].w, f, a.w));
             }
-            store_attention<D>(p, b, u / p.chunks * group + hc * HB + hd, d, a, M, l);
+            store_attention<D>(p, b, u / p.chunks * group + hc * HB + hd, d, a, M, log_sum(L, l));
         }
         __syncwarp();
         cluster_sync();  // no CTA leaves while another reads its piece
@@ -624,19 +681,20 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
 // pieces; the runs are joined through shared memory.  Bound by the latency of its dependent loads (which unit;
 // references and accumulators, eight pieces at a time).
 struct AttnPiece {
-    float M, l;
+    float M, L, l;  // references of the weights and of the sum
     float4 a;
-    __device__ __forceinline__ void add(float Mk, float lk, float4 v)  // the other's reference at most M
+    __device__ __forceinline__ void add(float Mk, float Lk, float4 v)  // the other's references at most M and L
     {
-        const float f = Mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : ex2(Mk - M);
-        l = fmaf(lk, f, l);
+        const float f = join_weight(Mk, Lk, M);
+        l += join_sum(Lk, L);
         a = make_float4(fmaf(v.x, f, a.x), fmaf(v.y, f, a.y), fmaf(v.z, f, a.z), fmaf(v.w, f, a.w));
     }
-    __device__ __forceinline__ void refer(float Mn)
+    __device__ __forceinline__ void refer(float Mn, float Ln)
     {
-        const float f = M == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(M - Mn);
+        const float f = join_weight(M, l == 0.f ? -INFINITY : 0.f, Mn);
+        l = l == 0.f ? 0.f : l * ex2_ftz(L - Ln);
         M = Mn;
-        l *= f;
+        L = Ln;
         a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
     }
 };
@@ -661,14 +719,14 @@ __global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(co
         const int k_begin = n * run / nr, k_end = run < nr ? n * (run + 1) / nr : 0;
         // the piece of CTA c is its last one, those of the CTAs behind their first
         const float *first = p.part + (2ll * c + 1) * PIECE, *rest = p.part + 2ll * c * PIECE;
-        AttnPiece all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        AttnPiece all{-INFINITY, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
         for (int k0 = k_begin; k0 < k_end; k0 += 8) {
             float2 ml[8];
             float4 v[8];
-            float M = all.M;
+            float M = all.M, L = all.L;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
+                ml[k] = make_float2(-INFINITY, -INFINITY);
                 v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k0 + k < k_end) {
                     const float *src = k0 + k == 0 ? first : rest + 2ll * (k0 + k) * PIECE;
@@ -677,8 +735,11 @@ __global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(co
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) M = fmaxf(M, ml[k].x);
-            all.refer(M);
+            for (int k = 0; k < 8; ++k) {
+                M = fmaxf(M, ml[k].x);
+                L = fmaxf(L, ml[k].y);
+            }
+            all.refer(M, L);
 #pragma unroll
             for (int k = 0; k < 8; ++k) all.add(ml[k].x, ml[k].y, v[k]);
         }
@@ -688,10 +749,11 @@ __global__ void __launch_bounds__(kAdJoinThreads) kda_attn_decode_join_kernel(co
         if (run > 0) return;
         for (int r = 1; r < nr; ++r) {
             const AttnPiece &o = runs[r * items + item];
-            all.refer(fmaxf(all.M, o.M));
-            all.add(o.M, o.l, o.a);
+            const float Lo = log_sum(o.L, o.l);
+            all.refer(fmaxf(all.M, o.M), fmaxf(all.L, Lo));
+            all.add(o.M, Lo, o.a);
         }
-        store_attention<D>(p, b, hk * group + hc * HB + hd, d, all.a, all.M, all.l);
+        store_attention<D>(p, b, hk * group + hc * HB + hd, d, all.a, all.M, log_sum(all.L, all.l));
     };
     const int4 out = p.shared_unit[2 * blockIdx.x], in = p.shared_unit[2 * blockIdx.x + 1];
     if (out.x >= 0) join(out, 0);

@@ -1,0 +1,92 @@
+"""The paged 8-bit cache on the GPU at the ends of its ranges: value scales, lengths.  Tolerances as in test_gpu_cache.py,
+whose formula in 64 bits this uses; a score of up to S is off by S * 2^-19 at most (fp32 sums of 128 products and its own
+rounding), which weighs p and lse."""
+import math
+
+import pytest
+import torch
+
+import kda_gated_delta_prefill_b200 as kda
+from tests.test_gpu_cache import BF16, E4M3, FP16, FP32, INT8, check_decode, formula, i32, make_decode
+
+pytestmark = pytest.mark.gpu
+
+
+def top_score(args, lens):
+    """The largest sum of |q| |k| over the dims, scaled: bounds every score."""
+    q, kc, _, ks, _, table = args
+    most = 0.0
+    for b, n in enumerate(lens):
+        ids = table[b, :-(-n // kc.shape[2])].long()
+        k = (kc.view(torch.uint8)[ids].view(kc.dtype).double() * ks[ids].double()[..., None, None]).nan_to_num()
+        qh = q[b].double().abs().view(kc.shape[1], -1, q.shape[2])
+        most = max(most, float((qh[None] @ k.abs().transpose(2, 3)).max()))
+    return most * q.shape[2] ** -0.5
+
+
+def check_scales(args, lens):
+    n = i32(lens)
+    o, lse = kda.attention_decode(*args, n)
+    f, z, w, tiny = formula(*args, lens, args[0].shape[2] ** -0.5)
+    slack = 2 * (FP32 + top_score(args, lens) * 2.0 ** -19)
+    assert ((lse.double() - z).abs() <= slack).all(), float((lse.double() - z).abs().max())
+    # (below 2^-126 bf16 has steps of 2^-133, and fp32 of 2^-149)
+    assert ((o.double() - f).abs() <= (FP16 + slack) * w + BF16 * f.abs() + tiny + 2.0 ** -134 + 2.0 ** -149).all()
+    assert kda.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("D,bs,H,HKV,n", [(128, 128, 8, 1, 70000), (64, 64, 16, 1, 131072), (128, 16, 2, 2, 3000),
+                                          (64, 32, 4, 2, 65536)])
+def test_decode_of_a_cache_of_zeros(dtype, D, bs, H, HKV, n):
+    """Zero keys and values as cache_append stores them, at scale 2^-100: o is 0 and lse the logarithm of the length."""
+    blocks = 4
+    kc, vc = (torch.ones(blocks, HKV, bs, D, device="cuda").to(dtype) for _ in range(2))
+    ks, vs = torch.ones(blocks, HKV, device="cuda"), torch.ones(blocks, HKV, device="cuda")
+    zero = torch.zeros(blocks * bs, HKV, D, dtype=torch.bfloat16, device="cuda")
+    kda.cache_append(zero, zero, kc, vc, ks, vs, torch.arange(blocks * bs, dtype=torch.int32, device="cuda"))
+    assert (vs == 2.0 ** -100).all()
+    table = (torch.arange(-(-n // bs), device="cuda") % blocks).to(torch.int32)[None].repeat(2, 1)
+    q = torch.randn(2, H, D, generator=torch.Generator("cuda").manual_seed(0), device="cuda").bfloat16()
+    lens = [n, n // 2 + 1]
+    o, lse = kda.attention_decode(q, kc, vc, ks, vs, table, i32(lens))
+    assert (o == 0).all()
+    want = torch.tensor([math.log(m) for m in lens], dtype=torch.float64, device="cuda")[:, None]
+    assert ((lse.double() - want).abs() < FP32).all(), lse
+    assert kda.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("D,bs", [(128, 16), (128, 64), (64, 16), (64, 128)])
+@pytest.mark.parametrize("lens,H,HKV,width", [([900, 40], 8, 2, None), ([9000, 300], 12, 1, None), ([900, 40], 8, 2, 2000)])
+@pytest.mark.parametrize("low,high", [(-120, -120), (-100, -5), (-120, 100), (-60, 60), (110, 110), (-149, -140)])
+def test_decode_of_any_value_scale(dtype, D, bs, lens, H, HKV, width, low, high):
+    """Value scales between 2^low and 2^high, block by block: alone, next to ordinary ones, and further apart than fp32's
+    exponents reach; in a narrow table (one launch) and in a wide one."""
+    args = list(make_decode(dtype, lens, H, HKV, D, bs, 21, width=width and width * 16 // bs))
+    g = torch.Generator("cuda").manual_seed(5)
+    some = torch.rand(args[4].shape, generator=g, device="cuda") < 0.5
+    args[4] = torch.tensor([2.0 ** high, 2.0 ** low], device="cuda")[some.long()]
+    check_scales(args, lens)
+
+
+@pytest.mark.parametrize("first,then", [(-100, 100), (100, -100)])
+def test_decode_of_value_scales_that_jump(first, then):
+    """Pieces of a unit whose scales are 2^200 apart: the sum of either counts in both."""
+    lens, H, HKV, D, bs = [60000], 4, 1, 128, 64
+    args = list(make_decode(E4M3, lens, H, HKV, D, bs, 22))
+    half = args[5][0, :400].long()
+    args[4].fill_(2.0 ** then)
+    args[4][half] = 2.0 ** first
+    check_scales(args, lens)
+
+
+def test_decode_of_all_scales_zero():
+    lens, H, HKV, D, bs = [500, 17], 4, 2, 64, 16
+    args = list(make_decode(E4M3, lens, H, HKV, D, bs, 23))
+    args[4].zero_()
+    o, lse = kda.attention_decode(*args, i32(lens))
+    assert (o == 0).all()
+    args[4].fill_(1.0)
+    check_decode(args, lens, *kda.attention_decode(*args, i32(lens)))
+    assert torch.equal(lse, kda.attention_decode(*args, i32(lens))[1])
