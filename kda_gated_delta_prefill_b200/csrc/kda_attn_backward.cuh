@@ -182,7 +182,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int rank = blockIdx.x % p.split, unit = blockIdx.x / p.split;
     const int hk = unit % p.HKV, G = p.H / p.HKV / p.split, head0 = (hk * p.split + rank) * G;
     int n, blk;
-    if (!pick_block<AT, false>(p.seq.cu_k, p.seq.N, p.seq.Tk, unit / p.HKV, lane, n, blk)) return;
+    if (!pick_block<AT, false>(p.seq.cu_k, p.seq.N, p.seq.Tk, unit / p.HKV, lane, n, blk)) {
+        // (where no sequence has a key, all CTAs leave here: dQ and what follows in the stream wait for this launch only)
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        return;
+    }
     const Seq sq = seq_of(p.seq, n);
     const int diff = sq.lk - sq.lq, j0 = blk * AT;
     // query tiles that see a key of this tile: first .. nq - 1 of each of this CTA's heads
