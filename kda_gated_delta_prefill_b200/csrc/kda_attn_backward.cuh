@@ -502,6 +502,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                                            ((static_cast<int64_t>(sq.k0) + j0 + row) * p.HKV + hk) * D + 4 * ch) =
                     make_uint2(pack_bf16(a.x * m, a.y * m), pack_bf16(a.z * m, a.w * m));
         }
+        __syncwarp();    // (an aligned barrier, and rows past the end took no part in the stores)
         cluster_sync();  // no CTA leaves while another reads its sums
     }
 }
