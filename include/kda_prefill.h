@@ -448,7 +448,10 @@ kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const v
  *   used         int32 [1] out: blocks taken
  * If free_blocks, the table's width or num_tokens do not suffice, the tokens
  * that miss a block get slot -1, table entries that miss one get -1, and bit 5
- * (32) of the device error word is set.  B <= 16384.
+ * (32) of the device error word is set.  A row that lacked blocks is planned
+ * anew from its length before: with the length after it, the entries of -1 count
+ * as blocks that it holds, and new tokens in them have slot -1 and set the bit
+ * again.  B <= 16384.
  *
  * kda_cache_append: rounds rows of k and v (bf16 [T, HKV, D], strided rows) to
  * codes in the slots of slot_map (-1: skipped).  The scale of a (block, head) is

@@ -631,7 +631,7 @@ def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num
     in place; free_blocks: int32 [F], taken from the front; num_tokens: the slot map's length, at least the sum of
     new_lens.  Returns (cu_seqlens [B+1], seq_lens [B], slot_map [num_tokens], used [1]), all int32: the new tokens'
     offsets, the lengths with them, each new token's slot (-1 behind the last), the number of blocks taken.  What does
-    not fit gets -1 and sets bit 5 of ``device_error``.
+    not fit gets -1 and sets bit 5 of ``device_error``; such a row is planned anew from its length before.
     """
     import torch
     if stream is not None:

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
     int steps = 0;
     while ((1 << steps) < p.B) ++steps;
     const bool wide = (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0;
+    bool lost = false;  // a token without a slot, also for want of a block in an earlier call
     for (int t = 4 * (blockIdx.x * kPlanThreads + tid); t < p.tokens; t += 4 * gridDim.x * kPlanThreads) {
         int slot[4] = {-1, -1, -1, -1};
         if (t < all.x) {
@@ -122,10 +123,12 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
                 const int s0 = place(row, pos);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) slot[j] = s0 < 0 ? -1 : s0 + j;
+                lost = lost || s0 < 0;
             } else {
                 for (int j = 0; j < 4 && t + j < all.x; ++j) {
                     while (cu[row + 1] <= t + j) ++row;
                     slot[j] = place(row, held[row] + t + j - cu[row]);
+                    lost = lost || slot[j] < 0;
                 }
             }
         }
@@ -135,6 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
             for (int j = 0; j < 4 && t + j < p.tokens; ++j) p.slot_map[t + j] = slot[j];
         }
     }
+    if (__any_sync(0xffffffffu, lost) && lane == 0) atomicOr(p.err, ERR_CACHE_FULL);
 }
 
 // ------------------------------------------------------------------------------------------ storing keys and values

@@ -90,3 +90,23 @@ def test_decode_of_all_scales_zero():
     args[4].fill_(1.0)
     check_decode(args, lens, *kda.attention_decode(*args, i32(lens)))
     assert torch.equal(lse, kda.attention_decode(*args, i32(lens))[1])
+
+
+def test_plan_reports_tokens_of_a_held_block_that_is_missing():
+    """What an earlier call could not supply stays missing when its lengths are carried on: its tokens have no slot, which
+    the error word says again; so do held entries and free blocks that name no block."""
+    table = i32([[3, -7, -7, -7], [5, -7, -7, -7]])
+    _, lens, slots, used = kda.cache_plan(i32([10, 16]), i32([30, 1]), table, i32([4]), 16, 31)
+    assert used.tolist() == [1] and table.tolist() == [[3, 4, -1, -7], [5, -1, -7, -7]]
+    assert slots.tolist() == [*range(58, 64), *range(64, 80), *[-1] * 9] and kda.device_error() == 32
+    _, lens, slots, used = kda.cache_plan(lens, i32([10, 0]), table, i32([8, 9]), 16, 10)
+    assert used.tolist() == [1] and lens.tolist() == [50, 17] and table.tolist() == [[3, 4, -1, 8], [5, -1, -7, -7]]
+    assert slots.tolist() == [-1] * 8 + [128, 129] and kda.device_error() == 32
+    kda.cache_plan(lens, i32([1, 0]), table, i32([8, 9]), 16, 1)  # the other row's block is not asked for
+    assert kda.device_error() == 0
+    _, _, slots, _ = kda.cache_plan(i32([20]), i32([13]), i32([[3, 1 << 30, 0]]), i32([-2]), 16, 13)
+    assert slots.tolist() == [-1] * 13 and kda.device_error() == 32
+    # from the length before the row is planned anew
+    _, lens, slots, used = kda.cache_plan(i32([32, 16]), i32([8, 1]), table, i32([6, 7]), 16, 9)
+    assert table.tolist() == [[3, 4, 6, 8], [5, 7, -7, -7]] and slots.tolist() == [*range(96, 104), 112]
+    assert kda.device_error() == 0
