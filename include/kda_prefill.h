@@ -437,7 +437,7 @@ kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const v
  * kda_cache_plan: block tables and slot maps on the device, from the lengths
  * alone, so a captured step needs no host round trip.  Row b holds
  * context_lens[b] tokens and gets new_lens[b] more (negative lengths count as
- * zero).  The blocks it lacks are taken from the front of free_blocks, row by
+ * zero, and lengths and offsets stop at 2^31 - 1).  The blocks it lacks are taken from the front of free_blocks, row by
  * row, and written into its table row behind those it has:
  *   block_table  int32 [B, table_width], rows table_stride elements apart, in/out
  *   cu_seqlens   int32 [B + 1] out: the new tokens' row offsets

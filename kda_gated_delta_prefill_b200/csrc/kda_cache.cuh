@@ -36,38 +36,38 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = 1 << p.shift, per = (p.B + kPlanThreads - 1) / kPlanThreads;
     auto blocks = [&](int tokens) { return (tokens >> p.shift) + ((tokens & (bs - 1)) != 0); };
+    // lengths, and sums of them and of blocks, stop at 2^31 - 1: no index below may come from a sum that wrapped
     auto ctx = [&](int b) { return max(p.context_lens[b], 0); };
-    auto add = [&](int b) { return max(p.new_lens[b], 0); };
+    auto add = [&](int b, int c) { return min(max(p.new_lens[b], 0), INT_MAX - c); };
+    auto sum = [](int x, int y) { return x > INT_MAX - y ? INT_MAX : x + y; };
     // this thread's rows b0 .. b1 - 1, then an exclusive scan over the threads
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int2 s = make_int2(0, 0);
     for (int b = b0; b < b1; ++b) {
-        const int c = ctx(b), a = add(b);
-        s.x += a;
-        s.y += blocks(c + a) - blocks(c);
+        const int c = ctx(b), a = add(b, c);
+        s.x = sum(s.x, a);
+        s.y = sum(s.y, blocks(c + a) - blocks(c));
     }
     int2 inc = s;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc.x, off), y = __shfl_up_sync(0xffffffffu, inc.y, off);
         if (lane >= off) {
-            inc.x += x;
-            inc.y += y;
+            inc.x = sum(inc.x, x);
+            inc.y = sum(inc.y, y);
         }
     }
     if (lane == 31) part[warp] = inc;
     __syncthreads();
-    int2 at = make_int2(inc.x - s.x, inc.y - s.y), all = make_int2(0, 0);
+    int2 at = make_int2(__shfl_up_sync(0xffffffffu, inc.x, 1), __shfl_up_sync(0xffffffffu, inc.y, 1));
+    if (lane == 0) at = make_int2(0, 0);
+    int2 all = make_int2(0, 0);
     for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) {
-            at.x += part[w].x;
-            at.y += part[w].y;
-        }
-        all.x += part[w].x;
-        all.y += part[w].y;
+        if (w == warp) at = make_int2(sum(all.x, at.x), sum(all.y, at.y));
+        all = make_int2(sum(all.x, part[w].x), sum(all.y, part[w].y));
     }
     for (int b = b0; b < b1; ++b) {
-        const int c = ctx(b), a = add(b);
+        const int c = ctx(b), a = add(b, c);
         cu[b] = at.x;
         take[b] = at.y;
         held[b] = c;
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
             p.cu_seqlens[b] = at.x;
             p.seq_lens[b] = c + a;
         }
-        at.x += a;
-        at.y += blocks(c + a) - blocks(c);
+        at.x = sum(at.x, a);
+        at.y = sum(at.y, blocks(c + a) - blocks(c));
     }
     if (tid == 0) {
         cu[p.B] = all.x;
@@ -90,11 +90,10 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
     // new table entries: a warp per row
     const int warps = gridDim.x * (kPlanThreads / 32);
     for (int b = blockIdx.x * (kPlanThreads / 32) + warp; b < p.B; b += warps) {
-        const int have = blocks(ctx(b)), need = blocks(ctx(b) + add(b));
+        const int have = blocks(ctx(b)), need = blocks(ctx(b) + add(b, ctx(b))), left = p.num_free - take[b];
         if (need > p.width && lane == 0) atomicOr(p.err, ERR_CACHE_FULL);
         for (int k = have + lane; k < min(need, p.width); k += 32) {
-            const int f = take[b] + k - have;
-            p.block_table[b * p.table_stride + k] = f < p.num_free ? p.free_blocks[f] : -1;
+            p.block_table[b * p.table_stride + k] = k - have < left ? p.free_blocks[take[b] + k - have] : -1;
         }
     }
     // The slot of each token; -1 behind the last one, and where there is no block.  A thread takes four tokens: one
@@ -112,10 +111,10 @@ __global__ void __launch_bounds__(kPlanThreads) kda_cache_plan_kernel(const Cach
             auto place = [&](int r, int pos) {
                 const int k = pos >> p.shift;
                 if (k >= p.width) return -1;
-                const int have = blocks(held[r]), f = take[r] + k - have;
-                const int id = k < have ? p.block_table[r * p.table_stride + k]
-                               : f < p.num_free ? p.free_blocks[f]
-                                                : -1;
+                const int have = blocks(held[r]), more = k - have;
+                const int id = more < 0                        ? p.block_table[r * p.table_stride + k]
+                               : more < p.num_free - take[r] ? p.free_blocks[take[r] + more]
+                                                             : -1;
                 return id >= 0 && id <= (INT_MAX >> p.shift) ? (id << p.shift) + (pos & (bs - 1)) : -1;
             };
             const int pos = held[row] + t - cu[row];

@@ -110,3 +110,24 @@ def test_plan_reports_tokens_of_a_held_block_that_is_missing():
     _, lens, slots, used = kda.cache_plan(i32([32, 16]), i32([8, 1]), table, i32([6, 7]), 16, 9)
     assert table.tolist() == [[3, 4, 6, 8], [5, 7, -7, -7]] and slots.tolist() == [*range(96, 104), 112]
     assert kda.device_error() == 0
+
+
+def test_plan_of_lengths_whose_sums_pass_32_bits():
+    """Lengths that are no lengths (of a row not in use, say) give no slot and no block of another row: sums stop at
+    2^31 - 1."""
+    top = 2 ** 31 - 1
+    table = i32([[1, 2], [-7, -7]])
+    cu, lens, slots, used = kda.cache_plan(i32([top, 0]), i32([1, 20]), table, i32([4, 5]), 16, 20)
+    assert cu.tolist() == [0, 0, 20] and lens.tolist() == [top, 20] and used.tolist() == [2]
+    assert table.tolist() == [[1, 2], [4, 5]] and slots.tolist() == list(range(64, 84)) and kda.device_error() == 32
+    table = i32([[-7], [3], [-7]])
+    cu, lens, slots, used = kda.cache_plan(i32([0, 5, 0]), i32([top, top, 7]), table, i32([4, 5, 6]), 16, 40)
+    assert cu.tolist() == [0, top, top, top] and lens.tolist() == [top, top, 7] and used.tolist() == [3]
+    assert table.tolist() == [[4], [3], [-1]] and slots.tolist() == [*range(64, 80), *[-1] * 24]
+    assert kda.device_error() == 32
+    rows = 700  # blocks, too, pass 2^31
+    table = torch.full((rows, 3), -7, dtype=torch.int32, device="cuda")
+    cu, lens, slots, used = kda.cache_plan(i32([0] * rows), i32([17] + [top] * (rows - 1)), table, i32([9, 8, 7, 6]), 16, 50)
+    assert cu[:3].tolist() == [0, 17, top] and (cu[2:] == top).all() and used.tolist() == [4]
+    assert table[:2].tolist() == [[9, 8, -7], [7, 6, -1]] and (table[2:] == -1).all()
+    assert slots.tolist() == [*range(144, 160), 128, *range(112, 128), *range(96, 112), -1] and kda.device_error() == 32
