@@ -444,7 +444,7 @@ kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const v
  *   seq_lens     int32 [B] out: context_lens + new_lens
  *   slot_map     int32 [num_tokens] out: each new token's slot, packed as
  *                cu_seqlens says, -1 behind the last one (num_tokens is the
- *                caller's bound on their number)
+ *                caller's bound on their number, below 2^31 - 2^20)
  *   used         int32 [1] out: blocks taken
  * If free_blocks, the table's width or num_tokens do not suffice, the tokens
  * that miss a block get slot -1, table entries that miss one get -1, and bit 5

@@ -642,6 +642,8 @@ def cache_plan(context_lens, new_lens, block_table, free_blocks, block_size, num
         raise ValueError("block_table must be [B, width]")
     if num_tokens < 0:
         raise ValueError("num_tokens must not be negative")
+    if num_tokens >= 1 << 31:
+        raise ValueError("num_tokens must be below 2^31")
     width = block_table.shape[1]
     dev = context_lens.device
     i32 = torch.int32

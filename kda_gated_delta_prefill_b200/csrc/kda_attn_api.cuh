@@ -317,7 +317,8 @@ extern "C" kda_status_t kda_cache_plan(const int32_t *context_lens, const int32_
 {
     if (B <= 0 || table_width <= 0 || num_free < 0 || num_tokens < 0) return KDA_ERR_INVALID_ARG;
     const int shift = block_shift(block_size);
-    if (shift < 0 || B > kda::kPlanMaxRows) return KDA_ERR_UNSUPPORTED;
+    // (the kernel's token index goes a step, 2,048 tokens a CTA, past the last token)
+    if (shift < 0 || B > kda::kPlanMaxRows || num_tokens > INT_MAX - (1 << 20)) return KDA_ERR_UNSUPPORTED;
     if (table_stride < table_width) return KDA_ERR_INVALID_ARG;
     if (!context_lens || !new_lens || !block_table || (num_free && !free_blocks) || !cu_seqlens || !seq_lens ||
         (num_tokens && !slot_map) || !used)
