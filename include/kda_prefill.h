@@ -484,7 +484,7 @@ kda_status_t kda_cache_append(const void *k, int64_t k_row_stride, const void *v
  *   workspace  16-byte aligned, kda_attention_decode_workspace_size(...) bytes;
  *        overlaps nothing else; calls that may run at the same time need their own
  * A row of length 0 (or less) gets o = 0 and lse = -inf.  Tokens whose block is out of
- * range do not count, a length past the table is cut off at it, and either sets
+ * range do not count, a length past the table or 2^31 - 4096 is cut off, and either sets
  * bit 4 (16) of the device error word.  What a block holds behind the last token
  * does not matter.  Value scales are positive; a block whose value scale is not
  * counts as zeros.  The same bits on every run.

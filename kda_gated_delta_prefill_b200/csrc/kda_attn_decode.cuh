@@ -46,6 +46,8 @@ constexpr int kAdWarps = 4, kAdThreads = 32 * kAdWarps + 32, kAdMaxCtas = 512;
 // D = 128; us on the device with a cluster and without: 500 tokens 5.4, 8.5; 2,000: 7.1, 10.2; 8,000: 13, 15; 32,000:
 // 37, 21).
 constexpr int kAdCluster = 8, kAdClusterTiles = 128;
+// The longest request: token indices, rounded up to tiles and looked up ahead, stay below 2^31.
+constexpr int kAdMaxTokens = INT_MAX - 4095;
 // The join's threads, and the pieces times float4s of a unit that it joins in one CTA: eight for each thread.
 constexpr int kAdJoinThreads = 512, kAdJoinItems = 8 * kAdJoinThreads;
 
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(kAdThreads, ad_ctas(NT))
     const int c = blockIdx.x;
     const int units_row = p.HKV * p.chunks, group = p.H / p.HKV;
     const int bs = 1 << shift;
-    const int cap = static_cast<int>(min(static_cast<int64_t>(p.width) << shift, static_cast<int64_t>(INT_MAX) - 64));
+    // (lengths are rounded up to tiles, and a batch of tiles, 512 tokens, is looked up ahead)
+    const int cap = static_cast<int>(min(static_cast<int64_t>(p.width) << shift, static_cast<int64_t>(kAdMaxTokens)));
     const uint32_t full0 = sb + S::BAR, empty0 = full0 + 8 * NST, qfull0 = empty0 + 8 * NST, qempty0 = qfull0 + 16;
     float4 *meta = reinterpret_cast<float4 *>(sm + S::META);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + S::ABORT);

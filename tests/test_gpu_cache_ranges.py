@@ -131,3 +131,17 @@ def test_plan_of_lengths_whose_sums_pass_32_bits():
     assert cu[:3].tolist() == [0, 17, top] and (cu[2:] == top).all() and used.tolist() == [4]
     assert table[:2].tolist() == [[9, 8, -7], [7, 6, -1]] and (table[2:] == -1).all()
     assert slots.tolist() == [*range(144, 160), 128, *range(112, 128), *range(96, 112), -1] and kda.device_error() == 32
+
+
+def test_decode_of_a_length_near_2_31():
+    """One block, 2^24 times in a row of the table.  444 CTAs take 37,800 tiles each, and a lane adds two terms a tile to its
+    sums, which rounds them by 2^-24 of themselves at most: 75,600 * 2^-24 < 2^-7."""
+    H, D, bs, width = 2, 64, 128, 1 << 24
+    q, kc, vc, ks, vs, _ = make_decode(INT8, [128], H, 1, D, bs, 31)
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    f, z, w, _ = formula(q, kc, vc, ks, vs, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), [128], D ** -0.5)
+    for n, cut, err in ((2 ** 31 - 4096, 0, 0), (2 ** 31 - 64, 4032, 16), (2 ** 31 - 1, 4095, 16)):
+        o, lse = kda.attention_decode(q, kc, vc, ks, vs, table, i32([n]))
+        assert kda.device_error() == err
+        assert ((lse.double() - z - math.log((n - cut) / 128)).abs() < 2.0 ** -7).all()
+        assert ((o.double() - f).abs() <= (2.0 ** -6 + FP16) * w + BF16 * f.abs()).all()
