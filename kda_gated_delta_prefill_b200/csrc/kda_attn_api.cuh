@@ -137,15 +137,16 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
 
 namespace {
 
-// CTAs (a cluster) that share the query heads of a key tile: as long as they fill the SMs in one wave.  With fewer CTAs
-// than SMs a key tile's loop over all heads of its group is the longest chain there is; with more than a wave of them
-// the clusters cost more than they balance (D = 128, 32/8 heads; us per backward with 1, 2 and 4 CTAs):
-//   512 tokens (32 key tiles): 41, 33, 32    1,024 (64): 69, 52, 60    2,048 (128): 133, 140, 161
-// and 8/1 heads, 2,048 tokens (16 key tiles): 232, 131, 72 and, with 8, 47.
+// CTAs (a cluster) that share the query heads of a key tile: until there are twice as many as SMs.  With fewer a key
+// tile's loop over all heads of its group is the longest chain there is; with more the clusters cost more than they
+// balance (D = 128, 32/8 heads; us per backward with 1, 2 and 4 CTAs):
+//   512 tokens (32 key tiles): 53, 47, 41    1,024 (64): 110, 80, 80    2,048 (128): 182, 150, 172
+// 16/4 heads, 4,096 tokens (128): 307, 219, 250, and 8,192 (256): 762, 782, 860; 8/1 heads, 2,048 tokens (16 key tiles): 240,
+// 176, 108 and, with 8, 76.
 int backward_split(int group, int64_t units, int sms)
 {
     int split = 1;
-    while (split < 8 && group % (2 * split) == 0 && 2 * split * units <= sms) split *= 2;
+    while (split < 8 && group % (2 * split) == 0 && split * units <= sms) split *= 2;
     return split;
 }
 
@@ -227,7 +228,7 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     if (!d.krows) mk = mv = mq;
     p.split = backward_split(H / HKV, static_cast<int64_t>(p.kslots) * HKV, info.sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // dK/dV is set up while the statistics are formed, and dQ fills the SMs that dK/dV leaves idle at its end
+    // a launch is set up while the one before it ends, where SMs are idle
     auto launch = [&](auto kern, int64_t grid, int smem, int cluster, bool early) {
         if (grid > INT_MAX) return KDA_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -259,8 +260,9 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
             stats<<<static_cast<int>(grid), kAttnStatThreads, 0, s>>>(p);
             if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
         }
-        if (d.krows) r = launch(dkv, static_cast<int64_t>(p.kslots) * HKV * p.split, dkv_smem, p.split, d.rows > 0);
-        if (r == KDA_OK && d.rows) r = launch(dqk, static_cast<int64_t>(p.qslots) * H, dq_smem, 1, d.krows > 0);
+        if (d.rows) r = launch(dqk, static_cast<int64_t>(p.qslots) * H, dq_smem, 1, true);
+        if (r == KDA_OK && d.krows)
+            r = launch(dkv, static_cast<int64_t>(p.kslots) * HKV * p.split, dkv_smem, p.split, d.rows > 0);
         return r;
     };
     return D == 128 ? run(kda_attn_stats_kernel<128>, kda_attn_dkv_kernel<128>, AttnDkvSmem<128>::TOTAL,

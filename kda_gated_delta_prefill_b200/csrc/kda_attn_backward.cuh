@@ -6,17 +6,20 @@
 //   dQ_i = scale sum_j dS_ij k_j    dK_j = scale sum_i dS_ij q_i
 // dK and dV of a shared key/value head are sums over its query heads.
 //
-// Three launches: the statistics (delta, and lse in units of log 2, in tiles of 128 rows), dK/dV, and dQ.  dK/dV walks
+// Three launches: the statistics (delta, and lse in units of log 2, in tiles of 128 rows), dQ, and dK/dV.  dK/dV walks
 // the queries for a tile of keys and dQ the keys for a tile of queries, so every sum has one owner and a fixed
 // order: no atomics, the same bits every time.  The price is that S and dP are formed twice (7 matrix products
 // instead of 5).
 //
-// Precision.  P and dS are rounded to bf16 for the products (2^-9 relative), and delta inherits the rounding of o:
-// where one key has most of a row's probability, dP_ij - delta_i is a small difference of it.  Rows that see at most 16
-// keys get delta in fp32 from its definition instead (statistics, below).  dQ and dK are 2.5e-3 off for scores of unit
-// variance and up to 5e-3 where the softmax over many keys is all but one-hot (of the 2-norm; 1.7e-3 is bf16 results
-// alone).  Delta from the row sums of dS, which should be zero, was measured: 2.5e-3 throughout, but dK/dV then has to
-// follow dQ, and a backward took 15-40 % longer.
+// Precision.  P and dS are rounded to bf16 for the products (2^-9 relative).  o . do inherits the rounding of o and of the
+// P that formed it, and where one key has most of a row's probability, dP_ij - delta_i is a small difference of it: dQ and
+// dK would be 2e-2 to 1.1 (of the 2-norm) off for probabilities of 0.96 to 0.9998.  But sum_j dS_ij is zero, so what dQ finds
+// it to be is delta's error.  dQ leaves the corrected delta for dK/dV, and corrects itself by taking the sum out at the key
+// whose P_ij is above 1/2 (at most one; without one, delta's error counts for little).  Rows that see at most 16 keys get
+// delta in fp32 from its definition (statistics, below).  dQ and dK are 2.4e-3 off for scores of unit variance and 2e-3 to
+// 5e-3 for those rows (1.7e-3 is bf16 results alone).  It costs 5 % (D = 128) and 8 % (D = 64) of the dQ kernel, and dQ has
+// to come first, where behind dK/dV it filled the SMs that the last key tiles leave idle: 2,675 -> 2,802 us for 16,384
+// tokens of 16/4 heads, 709 -> 760 for 8,192, 125 -> 150 for 2,048 of 32/8.
 //
 // dK/dV works on the transposes: a thread owns a key row of S^T = K Q^T and dP^T = V dO^T, so P^T and dS^T go back to
 // TMEM in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q; only Q and dO tiles move through shared memory.
@@ -28,10 +31,9 @@
 // sum still has one order (8,192 tokens, 16/16 heads: 327 -> 291 us).  At D = 128 that is slower (1,600 -> 1,750 us for
 // 16,384 tokens of 16/4 heads): dP and dK come between dV and S, which are the longest chain.
 //
-// The launches depend on one another on the device only as far as they have to: dK/dV sets up while the statistics are
-// formed, and dQ starts where SMs are idle at dK/dV's end (4,096 tokens, 16/4 heads: 345 -> 246 us).  Where key tiles
-// are few, a cluster of CTAs shares the heads of a group and adds up over distributed shared memory, in the CTAs'
-// order.
+// The launches depend on one another on the device only as far as they have to: each is set up while the one before it
+// ends.  Where key tiles are few, a cluster of CTAs shares the heads of a group and adds up over distributed shared memory,
+// in the CTAs' order.
 #pragma once
 #include "kda_attn_common.cuh"
 
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int hk = unit % p.HKV, G = p.H / p.HKV / p.split, head0 = (hk * p.split + rank) * G;
     int n, blk;
     if (!pick_block<AT, false>(p.seq.cu_k, p.seq.N, p.seq.Tk, unit / p.HKV, lane, n, blk)) {
-        // (where no sequence has a key, all CTAs leave here: dQ and what follows in the stream wait for this launch only)
+        // (where no sequence has a key, all CTAs leave here: what follows in the stream waits for this launch only)
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
     }
@@ -343,15 +345,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     } else {
         ATTN_BWD_FEWER_REGISTERS();
         if (warp == kAttnBwdLoad + 1 && lane == 0) {
-            // (also in CTAs without work.)  The statistics are complete behind the wait, so dQ may start, where SMs are
-            // idle
+            // (also in CTAs without work: what follows in the stream waits for this launch only)
             asm volatile("griddepcontrol.wait;\n" ::: "memory");
-            asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
         }
         if (warp == kAttnBwdLoad && lane == 0 && total > 0) {
             // ---------------- loads ----------------
-            // the statistics (nothing else depends on that launch)
-            asm volatile("griddepcontrol.wait;\n" ::: "memory");
             int nqi = 0, ndo = 0;  // tiles of Q and of dO requested
             bool ok = true;
             auto tile = [&](const CUtensorMap *m, uint32_t dst, int head, int row, uint32_t bar) {
@@ -359,6 +357,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             };
             mbar_expect_tx(kfull, TILE);
             tile(&mk, sb, hk, sq.k0 + j0, kfull);
+            mbar_expect_tx(vfull, TILE);
+            tile(&mv, sb + TILE, hk, sq.k0 + j0, vfull);
+            // the statistics, with dQ's corrections (nothing else depends on that launch)
+            asm volatile("griddepcontrol.wait;\n" ::: "memory");
             for (int it = 0, hq = head0, i = first; it < total && ok && !*abort_flag; ++it) {
                 const int st = it % NST;
                 const uint32_t par = ((it / NST) - 1) & 1;
@@ -371,10 +373,6 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 bulk_load(sb + S::STAT + st * 1024,
                           p.stats + (static_cast<int64_t>(hq) * p.qslots + qslot0 + i) * (2 * AT), 1024, qfull + 8 * st);
                 ++nqi;
-                if (it == 0) {
-                    mbar_expect_tx(vfull, TILE);
-                    tile(&mv, sb + TILE, hk, sq.k0 + j0, vfull);
-                }
                 if (it >= NST && !mbar_wait(doempty + 8 * st, par)) {
                     ok = false;
                     break;
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             if (!ok) fail(ERR_PIPE_EMPTY_WAIT);
             if (!ok || *abort_flag) {  // let the copies in flight land before the CTA leaves
                 mbar_wait(kfull, 0);
-                if (nqi) mbar_wait(vfull, 0);
+                mbar_wait(vfull, 0);
                 for (int i = max(0, nqi - NST); i < nqi; ++i) mbar_wait(qfull + 8 * (i % NST), (i / NST) & 1);
                 for (int i = max(0, ndo - NST); i < ndo; ++i) mbar_wait(dofull + 8 * (i % NST), (i / NST) & 1);
             }
@@ -539,13 +537,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H;
     int n, blk;
-    // dQ may start while dK/dV runs and has no use for it, but what follows in the stream waits for this launch only:
-    // the last CTA stays until dK/dV is complete
-    auto linger = [] {
-        if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    };
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (!pick_block<AT, true>(p.seq.cu_q, p.seq.N, p.seq.T, blockIdx.x / p.H, lane, n, blk)) {
-        linger();
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (what follows waits for this launch only)
         return;
     }
     const Seq sq = seq_of(p.seq, n);
@@ -583,11 +577,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const uint32_t td = tmem + lb + TM_DP + 32 * group;
         const int r = 32 * quarter + lane;
         const int slot = (p.seq.cu_q ? sq.q0 / AT + n : n * ((sq.lq + AT - 1) / AT)) + blk;
-        const float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
+        float *stat = p.stats + (static_cast<int64_t>(h) * p.qslots + slot) * (2 * AT);
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
         const float2 l2 = make_float2(stat[r], stat[r]), delta = make_float2(stat[AT + r], stat[AT + r]);
         // keys of this group that the row sees (rows past the end: p = 0)
         const int seen = r0 + r + 1 + diff - 32 * group;
         const float c = p.scale_log2;
+        float2 sum = make_float2(0.f, 0.f);  // of dS over this thread's keys
+        int best = -1;                       // the key whose probability is above 1/2, if it is one of them
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
             const uint32_t ts = tmem + lb + TM_S + 128 * (j & 1) + 32 * group;
@@ -610,6 +607,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                                       make_float2(c, c), l2);
                 pr[e] = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
             }
+            float top = fmaxf(pr[0].x, pr[0].y);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = max3(top, pr[e].x, pr[e].y);
+            if (__any_sync(0xffffffffu, top > 0.5f)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if ((e & 1 ? pr[e >> 1].y : pr[e >> 1].x) > 0.5f) best = j * AT + 32 * group + e;
+            }
             ok = __all_sync(0xffffffffu, mbar_wait_quiet(dpfull, j & 1));
             if (!ok) break;
             tc_fence_after();
@@ -623,6 +628,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             for (int e = 0; e < 16; ++e) {
                 const float2 a = mul2(pr[e], add2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                                   delta));
+                sum = add2(sum, a);
                 w[e] = pack_bf16(a.x, a.y);
             }
             tc_st16(ts, w);
@@ -632,14 +638,27 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             if (lane == 0) mbar_arrive(dsready0 + 8 * (j & 1));
         }
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait_quiet(done, 0));
+        // the rows' sums of dS over all keys (through the K tiles: no MMA reads them any more)
+        float *sums = reinterpret_cast<float *>(sm + S::K);
+        int *bests = reinterpret_cast<int *>(sums + 4 * AT);
+        if (ok) {
+            sums[group * AT + r] = sum.x + sum.y;
+            bests[group * AT + r] = best;
+        }
+        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kAttnBwdWarps) : "memory");
         if (!ok) {
             if (lane == 0) fail(ERR_PIPE_FULL_WAIT);
         } else if (group == 0) {
-            // through the Q tile (no MMA reads it any more)
+            const float off = (sums[r] + sums[AT + r]) + (sums[2 * AT + r] + sums[3 * AT + r]);
+            const int key = max(max(bests[r], bests[AT + r]), max(bests[2 * AT + r], bests[3 * AT + r]));
+            if (r0 + r < sq.lq) stat[AT + r] = delta.x - off;  // (a row behind them may hold anything)
+            // through the Q tile
             tc_fence_after();
-            const int row = r0 + 32 * quarter;
-            store_rows<D>(tmem + lb + TM_DQ, nt > 0, p.scale, sb + quarter * (32 * D * 2), lane, sq.lq - row,
-                          p.dq + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D, static_cast<int64_t>(p.H) * D);
+            const int row = r0 + 32 * quarter, hk = h / (p.H / p.HKV);
+            store_rows<D, true>(tmem + lb + TM_DQ, nt > 0, p.scale, sb + quarter * (32 * D * 2), lane, sq.lq - row,
+                                p.dq + ((static_cast<int64_t>(sq.q0) + row) * p.H + h) * D,
+                                static_cast<int64_t>(p.H) * D, -off,
+                                key < 0 ? nullptr : p.k + (static_cast<int64_t>(sq.k0) + key) * p.k_stride + hk * D);
         }
     } else {
         ATTN_BWD_FEWER_REGISTERS();
@@ -736,7 +755,6 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == kAttnBwdMma) tc_dealloc(tmem, TM_COLS);
-    linger();
 }
 
 }  // namespace kda

@@ -189,9 +189,11 @@ __device__ __forceinline__ bool find_block(const int32_t *cu, int N, int T, int 
 // The warp's 32 rows of a [128 rows][D] fp32 accumulator (TMEM, row = lane), times mul, rounded to bf16 and stored
 // to dst + row * stride for the first `rows` of them, through 32 * D * 2 bytes of shared memory so that the global
 // accesses are whole rows.  Without `any` the rows are zeros and TMEM is not read; a row whose mul is 0 is zeros.
-template <int D>
+// ADD: a row with an `other` row of D bf16 gets `weight` times that before the multiplication.
+template <int D, bool ADD = false>
 __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, uint32_t stage, int lane, int rows,
-                                           __nv_bfloat16 *dst, int64_t stride)
+                                           __nv_bfloat16 *dst, int64_t stride, float weight = 0.f,
+                                           const __nv_bfloat16 *other = nullptr)
 {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -199,6 +201,19 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, bool any, float mul, 
         if (any) {
             tc_ld32(taddr + 32 * i, v);
             tc_wait_ld();
+        }
+        if (ADD && other) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4 x = reinterpret_cast<const uint4 *>(other)[4 * i + e];
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[8 * e + 2 * k] = __float_as_uint(fmaf(bf16lo(u[k]), weight, __uint_as_float(v[8 * e + 2 * k])));
+                    v[8 * e + 2 * k + 1] =
+                        __float_as_uint(fmaf(bf16hi(u[k]), weight, __uint_as_float(v[8 * e + 2 * k + 1])));
+                }
+            }
         }
         const bool zero = !any || mul == 0.f;
 #pragma unroll
