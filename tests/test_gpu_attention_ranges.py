@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import kda_gated_delta_prefill_b200 as kda
-from tests.test_gpu_attention import HALF, cu_of, formula, heads
+from tests.test_gpu_attention import HALF, check_backward, check_forward, cu_of, formula, heads, sequences
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,45 @@ def test_gradients_of_one_key_among_packed_sequences_and_strided_rows():
         want = kda.attention_backward(*part[:3], oi, li, part[3])
         assert all(torch.equal(x[:, a:e], y) for x, y in zip(got, want))
     assert kda.device_error() == 0
+
+
+MIXED = [0, 1, 127, 128, 129, 255, 256, 257, 600, 64, 3, 40]
+RANGES = [
+    # T, H, HKV, D, lens, klens
+    (None, 2, 1, 64, [MIXED[i * 5 % 12] for i in range(150)], [MIXED[(i * 7 + 3) % 12] for i in range(150)]),  # the slot search
+    (None, 2, 2, 128, [MIXED[i * 5 % 12] for i in range(150)], None),
+    (None, 4, 2, 128, [MIXED[i * 7 % 12] for i in range(129)], [MIXED[(i * 7 + 1) % 12] for i in range(129)]),
+    (None, 2, 1, 128, [MIXED[i * 7 % 12] for i in range(128)], [MIXED[(i * 5 + 2) % 12] for i in range(128)]),  # levels
+    (None, 2, 1, 64, [MIXED[i * 7 % 12] for i in range(70)], None),
+    (None, 4, 1, 64, [MIXED[i * 11 % 12] for i in range(33)], [MIXED[(i * 11 + 5) % 12] for i in range(33)]),
+    (300, 8, 1, 128, None, None),    # eight CTAs to a key tile
+    (700, 16, 2, 64, None, None),
+    (700, 16, 2, 128, None, None),
+    (None, 8, 1, 64, [130, 300, 1], [300, 140, 20]),
+    (300, 24, 3, 128, None, None),
+    (200, 12, 1, 128, None, None),   # four of three heads
+    (6100, 2, 1, 128, None, None),   # long prompts
+    (9000, 1, 1, 64, None, None),
+    (None, 2, 2, 128, [5000, 3, 1300], [5500, 3, 1200]),
+]
+
+
+@pytest.mark.parametrize("T,H,HKV,D,lens,klens", RANGES)
+def test_many_sequences_and_heads_and_long_prompts_match_the_formula(T, H, HKV, D, lens, klens):
+    T = sum(lens) if T is None else T
+    Tk = T if klens is None else sum(klens)
+    q, k, v = heads(1, 1, T, H, D), heads(2, 1, Tk, HKV, D), heads(3, 1, Tk, HKV, D)
+    dout = heads(4, 1, T, H, D, gain=0.0)
+    cu = None if lens is None else cu_of(lens)
+    cu_k = None if klens is None else cu_of(klens)
+    o, lse = kda.attention_forward(q, k, v, cu, cu_k)
+    grads = kda.attention_backward(q, k, v, o, lse, dout, cu, cu_k)
+    torch.cuda.synchronize()
+    assert kda.device_error() == 0
+    check_forward(q, k, v, o, lse, lens, klens)
+    check_backward(q, k, v, dout, grads, lens, klens)
+    for _, a, n, c, m in sequences(1, T, Tk, lens, klens):
+        if m == 0:
+            assert (grads[0][:, a:a + n] == 0).all()
+        if n == 0:
+            assert (grads[1][:, c:c + m] == 0).all() and (grads[2][:, c:c + m] == 0).all()
