@@ -111,7 +111,6 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
     p.seq = SeqView{cu_seqlens, cu_seqlens_k, d.N, T, Tk};
     p.H = H;
     p.HKV = HKV;
-    p.slots = block_slots<kAttnFwdRows>(d.N, T, d.packed);
     p.scale = scale;
     p.scale_log2 = scale * kLog2e;
     p.o = static_cast<__nv_bfloat16 *>(o);
@@ -124,7 +123,7 @@ extern "C" kda_status_t kda_attention_forward(const void *q, int64_t q_row_strid
     } else if (!attn_map(&mk, k, HKV, d.krows, k_row_stride, D) || !attn_map(&mv, v, HKV, d.krows, v_row_stride, D)) {
         return KDA_ERR_CUDA;
     }
-    const int grid = p.slots * H;
+    const int grid = block_slots<kAttnFwdRows>(d.N, T, d.packed) * H;
     auto launch = [&](auto kern, int smem) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return KDA_ERR_CUDA;
@@ -198,7 +197,7 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     p.H = H;
     p.HKV = HKV;
     p.qslots = block_slots<AT>(d.N, T, d.packed);
-    p.kslots = block_slots<AT>(d.N, Tk, d.packed);
+    const int64_t kunits = static_cast<int64_t>(block_slots<AT>(d.N, Tk, d.packed)) * HKV;  // key tiles of all heads
     p.scale = scale;
     p.scale_log2 = scale * kLog2e;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -226,7 +225,7 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
     // a side without rows: the kernels write zeros to the other side's gradients and load nothing
     if (!d.rows) mq = mdo = mk;
     if (!d.krows) mk = mv = mq;
-    p.split = backward_split(H / HKV, static_cast<int64_t>(p.kslots) * HKV, info.sms);
+    p.split = backward_split(H / HKV, kunits, info.sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     // a launch is set up while the one before it ends, where SMs are idle
     auto launch = [&](auto kern, int64_t grid, int smem, int cluster, bool early) {
@@ -262,7 +261,7 @@ extern "C" kda_status_t kda_attention_backward(const void *q, int64_t q_row_stri
         }
         if (d.rows) r = launch(dqk, static_cast<int64_t>(p.qslots) * H, dq_smem, 1, true);
         if (r == KDA_OK && d.krows)
-            r = launch(dkv, static_cast<int64_t>(p.kslots) * HKV * p.split, dkv_smem, p.split, d.rows > 0);
+            r = launch(dkv, kunits * p.split, dkv_smem, p.split, d.rows > 0);
         return r;
     };
     return D == 128 ? run(kda_attn_stats_kernel<128>, kda_attn_dkv_kernel<128>, AttnDkvSmem<128>::TOTAL,

@@ -41,8 +41,8 @@ namespace kda {
 
 struct AttnBwdParams {
     SeqView seq;
-    int H, HKV, qslots, kslots;  // slots of 128 rows of q and of k
-    int split;                   // CTAs (a cluster) that share a key tile's query heads
+    int H, HKV, qslots;  // slots of 128 rows of q
+    int split;           // CTAs (a cluster) that share a key tile's query heads
     float scale, scale_log2;
     const __nv_bfloat16 *q, *k, *v, *o, *dout;
     int64_t q_stride, k_stride, v_stride, do_stride;

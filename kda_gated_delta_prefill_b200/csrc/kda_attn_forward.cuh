@@ -35,7 +35,7 @@ namespace kda {
 
 struct AttnFwdParams {
     SeqView seq;
-    int H, HKV, slots;
+    int H, HKV;
     float scale, scale_log2;  // scale, scale * log2(e)
     __nv_bfloat16 *o;         // [rows, H, D]
     float *lse;               // [B, H, T] (packed: B = 1)
