@@ -234,7 +234,9 @@ kda_status_t kda_prefill_forward_noalloc(const void *q, const void *k, const voi
  * copies and pipeline stages are bounded (about one second); a wait that
  * gives up sets a bit here (1: input tile copy, 2: stage fill, 4: stage
  * release) and the kernel stops early instead of hanging; bit 8 means a
- * tensor-memory allocation did not start at column 0 (not expected to happen).  Synchronises the
+ * tensor-memory allocation did not start at column 0 (not expected to happen).  Two
+ * bits report values on the device that the paged cache's calls cannot serve (16: a block, slot or
+ * length out of range; 32: blocks, table entries or slots that do not suffice).  Synchronises the
  * device.  clear != 0 resets the word afterwards.
  */
 kda_status_t kda_prefill_device_error(unsigned *word, int clear);
@@ -400,6 +402,8 @@ kda_status_t kda_l2norm_bf16(const void *x, int64_t rows, int K, void *out, void
  *   o             bf16 [B, T, H, D] out;  lse  fp32 [B, H, T] out.  Rows of no
  *                 sequence are left as they were, and what they hold (in q, k
  *                 and v) does not reach a result.
+ * Infinities and NaN inside a sequence may reach all of its rows, also those that
+ * do not see them (0 * NaN in a tile's matrix product).
  * Products are bf16 with fp32 accumulation; the softmax statistics are fp32.
  * T = 0 is a no-op.  No workspace.  Asynchronous on `stream`.
  */
@@ -410,7 +414,9 @@ kda_status_t kda_attention_forward(const void *q, int64_t q_row_stride, const vo
 
 /*
  * Gradients of sum(o * dout) for kda_attention_forward on the same inputs,
- * from the o and lse that it returned (lse itself carries no gradient):
+ * from the o and lse that it returned (lse itself carries no gradient; o and lse
+ * of attention over further keys, joined by their lse, do not do: a row's
+ * probabilities must sum to one over the keys given here):
  *   dq  bf16 [B, T, H, D];  dk, dv  bf16 [B, Tk, HKV, D], summed over the query
  *       heads that share a key/value head; rows of no sequence stay as they were
  *   dout  bf16, rows of [H, D] with a row stride, like q
@@ -460,7 +466,7 @@ kda_status_t kda_attention_backward(const void *q, int64_t q_row_stride, const v
  * becomes e4m3's NaN or int8's 0), and at least 2^-100.  Where the first of them does not
  * open the block, the scale is never smaller than it was, and when it grows, the
  * tokens before are rounded again.  Slots are unique; the tokens of one block
- * stand beside one another in ascending order.  Slots past the cache are
+ * stand beside one another in ascending order, none skipped between them.  Slots past the cache are
  * skipped and set bit 4 (16) of the device error word.
  * k_cache and v_cache may interleave in one allocation.
  */

@@ -397,7 +397,9 @@ def forward_host(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *, o, fi
 
 
 def device_error(clear: bool = True) -> int:
-    """Bits set by kernel waits that gave up on the current device (0 when none); synchronises."""
+    """Bits set on the current device (0 when none) by kernel waits that gave up (1, 2, 4, 8) and by the paged cache's
+    calls: 16, a block, slot or length out of range; 32, blocks, table entries or slots that do not suffice.
+    Synchronises."""
     w = ctypes.c_uint(0)
     _check(lib().kda_prefill_device_error(ctypes.byref(w), int(clear)), "kda_prefill_device_error")
     return int(w.value)
@@ -562,7 +564,8 @@ def attention_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None
     q: bf16 [B,T,H,D]; k, v: bf16 [B,Tk,HKV,D], H a multiple of HKV, D 64 or 128.  Rows are compact but may be
     strided (views of a packed QKV tensor).  Query i of a sequence with Lq queries and Lk keys sees the keys
     j <= i + Lk - Lq; a row that sees none gets o = 0 and lse = -inf.  Packed sequences: B = 1 and cu_seqlens int32
-    [N+1], with cu_seqlens_k where the keys' offsets differ; rows of no sequence are left as they were.
+    [N+1], with cu_seqlens_k where the keys' offsets differ; rows of no sequence are left as they were, and nothing of
+    them reaches a result (infinities and NaN inside a sequence may reach all of its rows).
     scale: D^-0.5 when not given.  lse is the natural logarithm of the row's sum of exponentials.
     """
     import torch
@@ -591,6 +594,7 @@ def attention_backward_workspace_size(B, T, H, num_seqs=0) -> int:
 def attention_backward(q, k, v, o, lse, dout, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, workspace=None,
                        stream=None):
     """Gradients of sum(o * dout) for ``attention_forward`` on the same inputs, from the o and lse it returned (CUDA).
+    (Not from those of attention over further keys: a row's probabilities must sum to one over the keys given here.)
 
     Returns (dq [B,T,H,D], dk, dv [B,Tk,HKV,D]) in bf16; dk and dv are summed over the query heads that share a
     key/value head.  dout's rows may be strided like q's.  Rows of no sequence are not written.
@@ -692,7 +696,7 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slot_map, *, stream=N
 
     k_cache, v_cache: torch.float8_e4m3fn or torch.int8 [num_blocks,HKV,block_size,D], compact inside a block;
     k_scale, v_scale: fp32 [num_blocks,HKV]; slot_map: int32 [T], -1 = skipped (see ``cache_plan``); slots are unique,
-    and the tokens of one block stand beside one another, in ascending order.  The scale of a (block, head) is the
+    and the tokens of one block stand beside one another, in ascending order, none skipped between them.  The scale of a (block, head) is the
     smallest power of two that its tokens fit; it grows, and the block's earlier tokens are rounded again, when later ones
     need it.
     """

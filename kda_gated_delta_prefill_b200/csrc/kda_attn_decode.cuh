@@ -4,14 +4,15 @@
 // with ks_b and vs_b the scales of token j's block and head.  Bound by reading the codes once: 2 D bytes per token and
 // key/value head.
 //
-// The work is cut evenly over the CTAs, whatever the lengths: the tiles of 64 tokens of all (row, key/value head)
+// The work is cut evenly over the CTAs, whatever the lengths: the tiles of all (row, key/value head)
 // units stand in one line of W, and CTA c of G <= W takes tiles [c W / G, (c + 1) W / G) of it.  A unit inside one CTA
 // is finished there; of a unit that several CTAs share, each leaves its maximum, sum and accumulator, and a second,
 // dependent launch joins them in the order of the CTAs.
 //
 // Few short requests take another form: a cluster of eight CTAs per unit, which join over distributed shared memory,
 // with no scan of the lengths and no second launch (one request of 777 tokens, 32/8 heads: 5.8 us on the device, 8.9 in
-// the other).
+// the other).  What the host knows of the lengths is the table's width: in a table wider than 128 tiles a short request
+// takes the first form.
 //
 // In a CTA, one warp requests the tiles' pages by TMA through a ring; four warps take 16 tokens of a tile each, with a
 // running softmax of their own, and join at the end of the unit.  All query heads of a group share one pass over the

@@ -21,10 +21,12 @@
 //    the other. A softmax warp that sees S may also rescale O: no MMA writes it then.
 //  D = 64: S of the next key tile is issued as soon as the softmax has read this one into registers, and each tile has
 //    its own issuer (0.69-0.75 ms for 16,384 tokens and 16 heads; 0.83 with P over S).
-// Bound at D = 64 by the exponentials (16 a cycle and SM: 2,048 cycles for both tiles, of about 2,700), and at D = 128,
-// for long sequences, by power: at 1,340 TFLOP/s the clock falls to 1.6 GHz.  Measured there without gain: a polynomial
-// on the FMA pipe for a quarter of the exponentials; scores in halves with N = 64, so that neither waits for the other
-// (fewer cycles, but Q read twice: less clock, 3.86 ms).  Waiting warps are suspended (mbarrier.try_wait): polling took
+// Bound at D = 64 by the exponentials (16 a cycle and SM: 2,048 cycles for both tiles, of about 2,700), and at D = 128 by
+// the chain from S to P to O and by power: for 32,768 tokens of 16/4 heads the tensor pipe is busy in 58 % of the cycles,
+// and back to back the clock falls to 1.59 GHz under the 1 kW limit (3.9 ms, 1,130 TFLOP/s; a single call on a rested card
+// 3.5 ms).  The pairs of times here were taken in turn on rested cards.  Measured without gain: a polynomial on the FMA
+// pipe for a quarter of the exponentials; scores in halves with N = 64, so that neither waits for the other (fewer cycles,
+// but Q read twice: less clock, 3.86 ms).  Waiting warps are suspended (mbarrier.try_wait): polling took
 // issue slots from the softmax (3.46 -> 3.36 ms).
 #pragma once
 #include <type_traits>
